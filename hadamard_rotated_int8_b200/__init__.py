@@ -16,29 +16,34 @@ The compute lives in ``libsdnq.so`` (hand-written CUDA behind the C ABI of
 * ``sdnq_gelu_bf16``            exact-erf GELU (MLP glue)
 * ``sdnq_rotquant_fp8``, ``sdnq_fp8_linear``  the FP8 (e4m3) variant of the same path
 * ``sdnq_attention_int8qk``     attention with Hadamard-rotated int8 QK and a bf16 PV
+* ``kv_cache``, ``sdnq_kv_write``, ``sdnq_kv_read``  a paged key/value cache in rotated int8
+* ``sdnq_attention_paged``      attention of new tokens (one, a few, a chunk) over that cache
 
 ``linear`` composes the online path (rotate + quantize, then the int8 linear).
 """
-from ._native import (SdnqError, lib, sdnq_attention_int8qk, sdnq_device_status,
+from ._native import (SdnqError, attention_paged_workspace, kv_cache, lib,
+                      sdnq_attention_int8qk, sdnq_attention_paged, sdnq_device_status,
                       sdnq_fp8_linear, sdnq_gelu_bf16,
                       sdnq_int8_linear, sdnq_rotquant_fp8,
                       sdnq_int8_grad_input_gemm, sdnq_int8_linear_fused,
                       sdnq_int8_linear_fused_plan, sdnq_int8_linear_gelu,
                       sdnq_int8_linear_grad_input, sdnq_int8_linear_lora,
                       sdnq_int8_linear_lora_noalloc, sdnq_int8_linear_lora_up,
-                      sdnq_lora_down, sdnq_rotate_quant_weight,
+                      sdnq_kv_read, sdnq_kv_write, sdnq_lora_down, sdnq_rotate_quant_weight,
                       sdnq_quant_grad_output, sdnq_rotquant_act, sdnq_selftest_wait_timeout,
                       status_string, version)
 
 __all__ = [
-    "SdnqError", "lib", "linear", "sdnq_attention_int8qk", "sdnq_device_status",
+    "SdnqError", "attention_paged_workspace", "kv_cache", "lib", "linear",
+    "sdnq_attention_int8qk", "sdnq_attention_paged", "sdnq_device_status",
     "sdnq_fp8_linear", "sdnq_gelu_bf16",
     "sdnq_int8_linear", "sdnq_rotquant_fp8",
     "sdnq_int8_grad_input_gemm", "sdnq_int8_linear_fused", "sdnq_int8_linear_fused_plan",
     "sdnq_int8_linear_gelu",
     "sdnq_int8_linear_grad_input",
     "sdnq_int8_linear_lora", "sdnq_quant_grad_output",
-    "sdnq_int8_linear_lora_noalloc", "sdnq_int8_linear_lora_up", "sdnq_lora_down",
+    "sdnq_int8_linear_lora_noalloc", "sdnq_int8_linear_lora_up", "sdnq_kv_read", "sdnq_kv_write",
+    "sdnq_lora_down",
     "sdnq_rotate_quant_weight", "sdnq_rotquant_act", "sdnq_selftest_wait_timeout",
     "status_string", "version",
 ]

@@ -26,6 +26,7 @@ SDNQ_ERR_ALIGN = 3
 SDNQ_ERR_UNSUPPORTED = 4
 SDNQ_ERR_CUDA = 5
 SDNQ_ERR_TIMEOUT = 6
+SDNQ_ERR_INDEX = 7
 
 MAX_K = 131072
 MIN_GROUP = 8
@@ -64,6 +65,11 @@ SIGNATURES = {
     "sdnq_attention_prep": [_P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _I32, _P, _I64, _P],
     "sdnq_attention_core": [_P, _I64, _I64, _I64, _I64, _I64, _F, _P, _I64, _P, _P],
     "sdnq_fp8_linear": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P],
+    "sdnq_kv_write": [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _I32, _P],
+    "sdnq_kv_read": [_P, _I64, _P, _P, _I64, _I32, _I64, _I64, _I32, _P, _I64, _P, _I64, _P],
+    "sdnq_attention_paged_workspace": [_I64, _I64, _I64],
+    "sdnq_attention_paged": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _P, _I64,
+                             _I32, _I64, _I64, _I64, _I32, _F, _I64, _I64, _P, _I64, _P, _I64, _P],
     "sdnq_device_status": [_P],
     "sdnq_selftest_wait_timeout": [_I64, _P],
     "sdnq_status_string": [ctypes.c_int],
@@ -100,6 +106,7 @@ def lib():
                     fn.argtypes = args
                     fn.restype = ctypes.c_char_p if name in ("sdnq_status_string",
                                                              "sdnq_version") else ctypes.c_int
+                cdll.sdnq_attention_paged_workspace.restype = _I64
                 _lib = cdll
     return _lib
 
@@ -568,6 +575,164 @@ def sdnq_gelu_bf16(x: torch.Tensor, out=None, stream=None):
     _mat(out, torch.bfloat16, M, N, "out")
     _check(lib().sdnq_gelu_bf16(_ptr(x), M, N, x.stride(0), _ptr(out), out.stride(0),
                                 _stream(stream)), "sdnq_gelu_bf16")
+    return out
+
+
+KV_MIN_PAGE = 16
+KV_MAX_PAGE = 256
+
+
+def _heads(t, name: str):
+    """Checks a [T, heads, D] bf16 tensor whose heads are dense within a token; returns
+    (T, heads, D, token stride)."""
+    _req(t, torch.bfloat16, name, 3)
+    T, H, D = t.shape
+    s0, s1, _ = t.stride()
+    if H > 1 and s1 != D:
+        raise ValueError(f"{name}: the heads of a token must be dense (stride {D}, got {s1})")
+    return T, H, D, s0 if T > 1 else (H * D + 7) // 8 * 8
+
+
+def _cache(codes, scales):
+    """Checks the two tensors of a paged cache; returns (pages, Hkv, page, D)."""
+    _req(codes, torch.int8, "codes", 5)
+    _req(scales, torch.float32, "scales", 4)
+    _dense(codes, "codes")
+    _dense(scales, "scales")
+    pages, Hkv, two, page, D = codes.shape
+    if two != 2:
+        raise ValueError(f"codes: expected shape [pages, Hkv, 2, page, D], got {tuple(codes.shape)}")
+    if scales.shape != (pages, Hkv, 2, page):
+        raise ValueError(f"scales: expected shape {(pages, Hkv, 2, page)}, got {tuple(scales.shape)}")
+    return pages, Hkv, page, D
+
+
+def _used_on(stream, *tensors):
+    """Tells torch's allocator that tensors made here (on the current stream) are used on
+    ``stream``, so that their memory is not handed out again before that work is done."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        t.record_stream(stream)
+
+
+def kv_cache(pages: int, Hkv: int, page: int, D: int, device=None):
+    """The two tensors of an empty paged cache: (codes [pages, Hkv, 2, page, D] int8, scales
+    [pages, Hkv, 2, page] fp32), zeroed, so that slots that were never written read as zeros."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return (torch.zeros((pages, Hkv, 2, page, D), dtype=torch.int8, device=device),
+            torch.zeros((pages, Hkv, 2, page), dtype=torch.float32, device=device))
+
+
+def sdnq_kv_write(k, v, slots, codes, scales, group: int = 256, stream=None):
+    """Quantizes k, v [T, Hkv, D] bf16 (rows of a wider tensor are fine) into slots [T] int64 of
+    the paged cache (codes, scales) in place. Negative slots leave their token out; the others
+    are distinct."""
+    T, Hkv, D, ldk = _heads(k, "k")
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    ldv = _heads(v, "v")[3]
+    pages, Hc, page, Dc = _cache(codes, scales)
+    if (Hkv, D) != (Hc, Dc):
+        raise ValueError(f"k: {Hkv} heads of {D}, but the cache has {Hc} heads of {Dc}")
+    _vec(slots, torch.int64, T, "slots")
+    if slots.numel() != T:
+        raise ValueError(f"slots: has {slots.numel()} elements, k has {T} tokens")
+    _check(lib().sdnq_kv_write(_ptr(k), ldk, _ptr(v), ldv, _ptr(slots), T, Hkv, D, group,
+                               _ptr(codes), _ptr(scales), pages, page, _stream(stream)),
+           "sdnq_kv_write")
+
+
+def sdnq_kv_read(slots, codes, scales, group: int = 256, k=None, v=None, stream=None):
+    """The rows of ``slots`` [T] int64 of the paged cache as (k, v) [T, Hkv, D] bf16, un-rotated.
+    A negative slot gives zeros."""
+    pages, Hkv, page, D = _cache(codes, scales)
+    _vec(slots, torch.int64, 0, "slots")
+    T = slots.numel()
+    made = []
+    if k is None:
+        k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=codes.device)
+        made.append(k)
+    if v is None:
+        v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=codes.device)
+        made.append(v)
+    ld = []
+    for t, n in ((k, "k"), (v, "v")):
+        ld.append(_heads(t, n)[3])
+        if t.shape != (T, Hkv, D):
+            raise ValueError(f"{n}: expected shape {(T, Hkv, D)}, got {tuple(t.shape)}")
+    _used_on(stream, *made)
+    _check(lib().sdnq_kv_read(_ptr(slots), T, _ptr(codes), _ptr(scales), pages, page, Hkv, D, group,
+                              _ptr(k), ld[0], _ptr(v), ld[1], _stream(stream)), "sdnq_kv_read")
+    return k, v
+
+
+_paged_ws_bytes: dict = {}
+
+
+def attention_paged_workspace(H: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace sdnq_attention_paged takes for these heads."""
+    total = _paged_ws_bytes.get((H, Hkv, D))
+    if total is None:
+        total = int(lib().sdnq_attention_paged_workspace(H, Hkv, D))
+        if total < 0:
+            raise ValueError(f"bad attention heads: {H} query heads, {Hkv} kv heads of {D}")
+        _paged_ws_bytes[(H, Hkv, D)] = total
+    return total
+
+
+def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int = 1,
+                         group: int = 256, scale: float | None = None, window: int = 0,
+                         sinks: int = 0, ws=None, out=None, stream=None):
+    """Attention of the new tokens q [T, H, D] bf16 of B sequences over their pages of the cache
+    (codes, scales): out [T, H, D] bf16. table [B, max_pages] int32 page ids, lens [B] int32
+    tokens in the cache (the new ones included), cu_q [B + 1] int32 row offsets of the sequences
+    (None: one new token each, T == B); max_q bounds the new tokens of a sequence. Causal; with
+    ``window`` > 0 a token sees the last ``window`` keys and the first ``sinks``. ``ws``: uint8,
+    attention_paged_workspace bytes."""
+    T, H, D, ldq = _heads(q, "q")
+    pages, Hkv, page, Dc = _cache(codes, scales)
+    if D != Dc or H % Hkv:
+        raise ValueError(f"q: {H} heads of {D} do not fit a cache of {Hkv} heads of {Dc}")
+    _req(table, torch.int32, "table", 2)
+    B, width = table.shape
+    _vec(lens, torch.int32, B, "lens")
+    if lens.numel() != B:
+        raise ValueError(f"lens: has {lens.numel()} elements, table has {B} rows")
+    if cu_q is None:
+        if T != B:
+            raise ValueError(f"q: {T} rows for {B} sequences of one token each (give cu_q)")
+    else:
+        _vec(cu_q, torch.int32, B + 1, "cu_q")
+        if cu_q.numel() != B + 1:
+            raise ValueError(f"cu_q: has {cu_q.numel()} elements, needs {B + 1}")
+    ldt = table.stride(0) if B > 1 else width
+    if ldt < width:
+        raise ValueError("table: rows overlap")
+    total = attention_paged_workspace(H, Hkv, D)
+    made = []
+    if ws is None:
+        ws = torch.empty(total, dtype=torch.uint8, device=q.device)
+        made.append(ws)
+    else:
+        _vec(ws, torch.uint8, total, "ws")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+        made.append(out)
+        ldo = H * D
+    else:
+        ldo = _heads(out, "out")[3]
+        if out.shape != q.shape:
+            raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    _used_on(stream, *made)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    _check(lib().sdnq_attention_paged(_ptr(q), ldq, T, H, _ptr(cu_q), _ptr(lens), B, _ptr(table),
+                                      width, ldt, _ptr(codes), _ptr(scales), pages, page, Hkv, D,
+                                      int(max_q), group, scale, int(window), int(sinks), _ptr(ws),
+                                      ws.numel(), _ptr(out), ldo, _stream(stream)),
+           "sdnq_attention_paged")
     return out
 
 

@@ -10,9 +10,10 @@
 
 namespace sdnq {
 
-// Device error word: set (never cleared) by a kernel whose bounded wait gave up; read and
-// cleared by the host through sdnq_device_status().
-enum : unsigned int { kDevOk = 0u, kDevTimeout = 1u };
+// Device error word: set (never cleared) by a kernel whose bounded wait gave up, or that found
+// a slot, page id, length or row offset out of range in the caller's device memory (and left
+// out what it names); read and cleared by the host through sdnq_device_status().
+enum : unsigned int { kDevOk = 0u, kDevTimeout = 1u, kDevIndex = 2u };
 __device__ unsigned int g_device_error = 0u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)

@@ -1,0 +1,231 @@
+// The paged key/value cache and the attention over it: validation and launches.
+//
+// This file is part of libsdnq.cu's translation unit (included at its end).
+
+#include "attention_paged.cuh"
+#include "kvcache.cuh"
+
+namespace sdnq {
+namespace {
+
+// Sizes shared by every call on a cache; codes and scales are required unless there is no work.
+sdnq_status validate_cache(const void *codes, const void *scales, int64_t pages, int32_t page,
+                           int64_t Hkv, int64_t D, int32_t group)
+{
+    if (pages < 0 || Hkv < 1 || Hkv > 65536)
+        return SDNQ_ERR_SHAPE;
+    if ((D != 64 && D != 128) || !is_pow2(page) || page < SDNQ_KV_MIN_PAGE ||
+        page > SDNQ_KV_MAX_PAGE || !is_pow2(group) || group < SDNQ_MIN_GROUP ||
+        group > SDNQ_MAX_GROUP)
+        return SDNQ_ERR_UNSUPPORTED;
+    // rows of the pool are numbered in 32 bits by the copy engine
+    if (pages > INT32_MAX / (2 * Hkv * page))
+        return SDNQ_ERR_SHAPE;
+    if (!aligned(codes, 16) || !aligned(scales, 16))
+        return SDNQ_ERR_ALIGN;
+    return SDNQ_OK;
+}
+
+int32_t log2_of(int64_t v)
+{
+    int32_t s = 0;
+    while ((1ll << s) < v)
+        ++s;
+    return s;
+}
+
+float rotation_factor(int64_t g) { return static_cast<float>(1.0 / std::sqrt(static_cast<double>(g))); }
+
+sdnq_status validate_kv_rows(const void *k, int64_t ldk, const void *v, int64_t ldv,
+                             const void *slots, int64_t T, int64_t Hkv, int64_t D, int32_t group,
+                             const void *codes, const void *scales, int64_t pages, int32_t page)
+{
+    if (T != 0 && (!k || !v || !slots || !codes || !scales))
+        return SDNQ_ERR_NULL;
+    if (T < 0 || T > INT32_MAX)
+        return SDNQ_ERR_SHAPE;
+    const sdnq_status st = validate_cache(codes, scales, pages, page, Hkv, D, group);
+    if (st != SDNQ_OK)
+        return st;
+    if (ldk < Hkv * D || ldv < Hkv * D)
+        return SDNQ_ERR_SHAPE;
+    if (ldk % 8 != 0 || ldv % 8 != 0 || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
+        return SDNQ_ERR_ALIGN;
+    return SDNQ_OK;
+}
+
+template <bool WRITE, int G, int D>
+void launch_kv(const KvParams &p, int sm_count, cudaStream_t cs)
+{
+    constexpr int rows_per_warp = 1024 / D;
+    const int64_t chunks = (p.rows + rows_per_warp - 1) / rows_per_warp;
+    int64_t blocks = (chunks + 7) / 8;
+    const int64_t most = static_cast<int64_t>(sm_count) * 8;
+    if (blocks > most)
+        blocks = most;
+    launch_programmatic(WRITE ? kv_write_kernel<G, D> : kv_read_kernel<G, D>,
+                        dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, p);
+}
+
+template <bool WRITE>
+sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int64_t *slots,
+                   int64_t T, int64_t Hkv, int64_t D, int32_t group, int8_t *codes, float *scales,
+                   int64_t pages, int32_t page, void *stream)
+{
+    sdnq_status st = validate_kv_rows(k, ldk, v, ldv, slots, T, Hkv, D, group, codes, scales, pages,
+                                      page);
+    if (st != SDNQ_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != SDNQ_OK)
+        return st;
+    if (T == 0)
+        return SDNQ_OK;
+    const int64_t g = group < D ? group : D;
+    KvParams p = {};
+    p.k = k;
+    p.v = v;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.slots = slots;
+    p.codes = codes;
+    p.scales = scales;
+    p.rows = T * 2 * Hkv;
+    p.nslots = pages * page;
+    p.Hkv = static_cast<int32_t>(Hkv);
+    p.page_shift = log2_of(page);
+    p.c_g = rotation_factor(g);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaGetLastError();
+    if (D == 128) {
+        switch (g) {
+        case 8: launch_kv<WRITE, 8, 128>(p, dev.sm_count, cs); break;
+        case 16: launch_kv<WRITE, 16, 128>(p, dev.sm_count, cs); break;
+        case 32: launch_kv<WRITE, 32, 128>(p, dev.sm_count, cs); break;
+        case 64: launch_kv<WRITE, 64, 128>(p, dev.sm_count, cs); break;
+        default: launch_kv<WRITE, 128, 128>(p, dev.sm_count, cs); break;
+        }
+    } else {
+        switch (g) {
+        case 8: launch_kv<WRITE, 8, 64>(p, dev.sm_count, cs); break;
+        case 16: launch_kv<WRITE, 16, 64>(p, dev.sm_count, cs); break;
+        case 32: launch_kv<WRITE, 32, 64>(p, dev.sm_count, cs); break;
+        default: launch_kv<WRITE, 64, 64>(p, dev.sm_count, cs); break;
+        }
+    }
+    return launch_status();
+}
+
+int64_t paged_workspace() { return 256; }
+
+// Largest context, window and sink count that the kernels' 32-bit positions hold.
+constexpr int64_t kPagedMaxKeys = 1ll << 30;
+
+sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,
+                                const int32_t *cu_q, const int32_t *lens, int64_t B,
+                                const int32_t *table, int64_t max_pages, int64_t ldt, const int8_t *codes,
+                                const float *scales, int64_t pages, int32_t page, int64_t Hkv,
+                                int64_t D, int64_t max_q, int32_t group, float scale,
+                                int64_t window, int64_t sinks, void *ws, int64_t ws_bytes,
+                                uint16_t *out, int64_t ldo, void *stream)
+{
+    const bool work = T != 0 && B != 0;
+    if (work && (!q || !lens || !table || !codes || !scales || !ws || !out))
+        return SDNQ_ERR_NULL;
+    if (T < 0 || B < 0 || T > INT32_MAX || B >= INT32_MAX || H < 1 || H > 65536 || max_q < 1 ||
+        window < 0 || sinks < 0 || max_pages < 0 || ldt < max_pages)
+        return SDNQ_ERR_SHAPE;
+    sdnq_status st = validate_cache(codes, scales, pages, page, Hkv, D, group);
+    if (st != SDNQ_OK)
+        return st;
+    if (H % Hkv != 0 || T * H > INT32_MAX || (cu_q == nullptr && T < B) ||
+        max_pages > kPagedMaxKeys / page || ldq < H * D || ldo < H * D)
+        return SDNQ_ERR_SHAPE;
+    if (!(scale >= 0.0f && scale <= FLT_MAX))
+        return SDNQ_ERR_UNSUPPORTED;
+    if (ldq % 8 != 0 || ldo % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
+        !aligned(lens, 4) || !aligned(table, 4) || !aligned(ws, 256))
+        return SDNQ_ERR_ALIGN;
+    if (work && ws_bytes < paged_workspace())
+        return SDNQ_ERR_SHAPE;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != SDNQ_OK)
+        return st;
+    if (!work)
+        return SDNQ_OK;
+    const int64_t g = group < D ? group : D;
+    PagedParams p = {};
+    p.q = q;
+    p.o = out;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.cu = cu_q;
+    p.lens = lens;
+    p.table = table;
+    p.table_ld = ldt;
+    p.codes = codes;
+    p.scales = scales;
+    p.pages = pages;
+    p.T = static_cast<int32_t>(T);
+    p.B = static_cast<int32_t>(B);
+    p.H = static_cast<int32_t>(H);
+    p.Hkv = static_cast<int32_t>(Hkv);
+    p.share = static_cast<int32_t>(H / Hkv);
+    p.page_shift = log2_of(page);
+    p.cap = static_cast<int32_t>(max_pages * page);
+    p.window = static_cast<int32_t>(window < kPagedMaxKeys ? window : kPagedMaxKeys);
+    p.sinks = static_cast<int32_t>(sinks < kPagedMaxKeys ? sinks : kPagedMaxKeys);
+    p.group = static_cast<int32_t>(g);
+    p.scale = scale;
+    p.c_g = rotation_factor(g);
+    cudaGetLastError();
+    const unsigned blocks = static_cast<unsigned>((T * H + 3) / 4);
+    launch_programmatic(D == 128 ? attn_paged_kernel<128> : attn_paged_kernel<64>, dim3(blocks),
+                        dim3(128), 0, static_cast<cudaStream_t>(stream), p);
+    return launch_status();
+}
+
+} // namespace
+} // namespace sdnq
+
+SDNQ_API sdnq_status sdnq_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                                   const int64_t *slots, int64_t T, int64_t Hkv, int64_t D,
+                                   int32_t group, int8_t *codes, float *scales, int64_t pages,
+                                   int32_t page, void *stream)
+{
+    SDNQ_NVTX_RANGE();
+    return run_kv<true>(const_cast<uint16_t *>(k), ldk, const_cast<uint16_t *>(v), ldv, slots, T,
+                        Hkv, D, group, codes, scales, pages, page, stream);
+}
+
+SDNQ_API sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes,
+                                  const float *scales, int64_t pages, int32_t page, int64_t Hkv,
+                                  int64_t D, int32_t group, uint16_t *k, int64_t ldk, uint16_t *v,
+                                  int64_t ldv, void *stream)
+{
+    SDNQ_NVTX_RANGE();
+    return run_kv<false>(k, ldk, v, ldv, slots, T, Hkv, D, group, const_cast<int8_t *>(codes),
+                         const_cast<float *>(scales), pages, page, stream);
+}
+
+SDNQ_API int64_t sdnq_attention_paged_workspace(int64_t H, int64_t Hkv, int64_t D)
+{
+    if (H < 1 || Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128))
+        return -1;
+    return sdnq::paged_workspace();
+}
+
+SDNQ_API sdnq_status sdnq_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,
+                                          const int32_t *cu_q, const int32_t *lens, int64_t B,
+                                          const int32_t *table, int64_t max_pages, int64_t ldt, const int8_t *codes,
+                                          const float *scales, int64_t pages, int32_t page,
+                                          int64_t Hkv, int64_t D, int64_t max_q, int32_t group,
+                                          float scale, int64_t window, int64_t sinks, void *ws,
+                                          int64_t ws_bytes, uint16_t *out, int64_t ldo,
+                                          void *stream)
+{
+    SDNQ_NVTX_RANGE();
+    return run_attention_paged(q, ldq, T, H, cu_q, lens, B, table, max_pages, ldt, codes, scales, pages, page,
+                               Hkv, D, max_q, group, scale, window, sinks, ws, ws_bytes, out, ldo,
+                               stream);
+}

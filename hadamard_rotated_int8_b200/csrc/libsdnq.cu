@@ -1398,7 +1398,7 @@ SDNQ_API sdnq_status sdnq_device_status(void *stream)
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) != cudaSuccess)
             return SDNQ_ERR_CUDA;
-        return SDNQ_ERR_TIMEOUT;
+        return (word & kDevTimeout) ? SDNQ_ERR_TIMEOUT : SDNQ_ERR_INDEX;
     }
     return SDNQ_OK;
 }
@@ -1445,6 +1445,7 @@ SDNQ_API const char *sdnq_status_string(sdnq_status s)
     case SDNQ_ERR_UNSUPPORTED: return "SDNQ_ERR_UNSUPPORTED: unsupported group/rank or device is not sm_100";
     case SDNQ_ERR_CUDA: return "SDNQ_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     case SDNQ_ERR_TIMEOUT: return "SDNQ_ERR_TIMEOUT: a bounded wait inside a kernel gave up";
+    case SDNQ_ERR_INDEX: return "SDNQ_ERR_INDEX: a slot, page id, length or row offset in device memory is out of range";
     }
     return "SDNQ_ERR_UNKNOWN";
 }
@@ -1453,3 +1454,5 @@ SDNQ_API const char *sdnq_version(void) { return "sdnq-b200 0.1.0 sm_100a"; }
 
 // The no-allocation LoRA variant (its own file; shares this translation unit).
 #include "lora_noalloc.cu"
+// The paged key/value cache (its own file; shares this translation unit).
+#include "kvcache.cu"

@@ -40,7 +40,8 @@
  *    launched when it is not SDNQ_OK, and outputs are then unspecified. Faults inside a
  *    kernel surface at the caller's next synchronisation.
  *  - Every bounded wait inside a kernel that gives up (default limit about 2 s) sets a
- *    device error word; sdnq_device_status() reads and clears it (SDNQ_ERR_TIMEOUT).
+ *    device error word; sdnq_device_status() reads and clears it (SDNQ_ERR_TIMEOUT). So
+ *    does an index in the caller's device memory that is out of range (SDNQ_ERR_INDEX).
  *  - Only sm_100 devices are supported (SDNQ_ERR_UNSUPPORTED otherwise). There is no CPU
  *    and no other-architecture path.
  *  - The int8 GEMMs, the attention kernel and the attention preparation are launched with
@@ -65,7 +66,9 @@ typedef enum {
     SDNQ_ERR_ALIGN = 3,       /* a pointer or leading dimension breaks the 16-byte rule    */
     SDNQ_ERR_UNSUPPORTED = 4, /* group size or rank not supported, or device is not sm_100 */
     SDNQ_ERR_CUDA = 5,        /* a CUDA runtime call or a kernel launch failed             */
-    SDNQ_ERR_TIMEOUT = 6      /* a bounded wait inside a kernel gave up                    */
+    SDNQ_ERR_TIMEOUT = 6,     /* a bounded wait inside a kernel gave up                    */
+    SDNQ_ERR_INDEX = 7        /* a slot, page id, length or row offset in device memory was
+                                 out of range: what it names was left out                  */
 } sdnq_status;
 
 /* Largest K accepted by every call (int32 accumulators stay exact: 127*127*K < 2^31). */
@@ -349,6 +352,80 @@ sdnq_status sdnq_attention_core(const uint16_t *v, int64_t B, int64_t Lq, int64_
                                 void *stream);
 
 /*
+ * The paged key/value cache in rotated int8, for decoding with the attention below. A page
+ * holds `page` tokens of every kv head, keys and values:
+ *   codes  [pages][Hkv][2][page][D] int8 (2: keys, then values), dense, 16-byte aligned;
+ *   scales [pages][Hkv][2][page] fp32, dense, 16-byte aligned;
+ *   page: a power of two, SDNQ_KV_MIN_PAGE..SDNQ_KV_MAX_PAGE; D: 64 or 128 (else
+ *   SDNQ_ERR_UNSUPPORTED); pages * Hkv * 2 * page < 2^31, Hkv <= 65536.
+ * A slot is page_id * page + offset. Which page belongs to which sequence is the caller's.
+ * Every call on one cache uses the same `group` (rotation groups of min(group, D)).
+ *
+ * sdnq_kv_write: quantizes the keys and values of T tokens into their slots, each (token,
+ *   head) row exactly as sdnq_rotquant_act quantizes a row of K = D with group min(group, D).
+ *   k, v [T][Hkv][D] bf16, the heads of a token dense, token strides ldk, ldv (>= Hkv * D,
+ *   multiples of 8), 16-byte aligned; so both may be parts of a fused projection's rows.
+ *   slots [T] int64. A negative slot leaves its token out; a slot past the pool does too, and
+ *   records SDNQ_ERR_INDEX. Slots that are not negative are distinct within a call: of two
+ *   tokens with one slot, which one's codes (or a mix) it holds afterwards is unspecified.
+ *   Rows with infinities or NaN: the codes and the scale are unspecified.
+ *
+ * sdnq_kv_read: the rows of T slots as bf16, x = bf16(butterfly(code) * fp32(s * c)) with
+ *   c = fp32(1/sqrt(min(group, D))). k, v [T][Hkv][D] out, strides as above. A negative slot
+ *   gives zeros; so does one past the pool, which records SDNQ_ERR_INDEX. Slots may repeat.
+ *
+ * T == 0 is a no-op.
+ */
+#define SDNQ_KV_MIN_PAGE 16
+#define SDNQ_KV_MAX_PAGE 256
+sdnq_status sdnq_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                          const int64_t *slots, int64_t T, int64_t Hkv, int64_t D, int32_t group,
+                          int8_t *codes, float *scales, int64_t pages, int32_t page, void *stream);
+sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, const float *scales,
+                         int64_t pages, int32_t page, int64_t Hkv, int64_t D, int32_t group,
+                         uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, void *stream);
+
+/*
+ * Attention of the new tokens of B sequences over their pages of that cache (their own keys
+ * and values are written first, with sdnq_kv_write): causal, grouped heads, optionally within
+ * a sliding window beside which the first `sinks` tokens stay visible.
+ *   q [T][H][D] bf16, token stride ldq (>= H * D, multiple of 8), 16-byte aligned; H a
+ *     multiple of Hkv, query head h reads kv head h / (H / Hkv); T * H < 2^31.
+ *   cu_q [B + 1] int32, not decreasing: rows cu_q[b] .. cu_q[b+1] - 1 of q are the new tokens
+ *     of sequence b (none is allowed). NULL: one new token each, row b is sequence b's.
+ *   lens [B] int32: tokens of the sequence in the cache, the new ones included.
+ *   table [B][max_pages] int32, row stride ldt >= max_pages: page ids of the sequence's tokens
+ *     in order; entries past its length are not read. max_pages * page <= 2^30. Sequences may
+ *     share pages.
+ * New token i of a sequence of length L with n new tokens is at position p = L - n + i and
+ * sees the keys j <= p with (window == 0 or j > p - window or j < sinks):
+ *   logit_j = (qc . kc_j) * (s_q * s_k[j]) * scale, qc and s_q the codes and scale of its q
+ *   row as sdnq_kv_write makes them; o = butterfly(sum_j softmax(logit)_j * s_v[j] * vc_j) * c.
+ *   Probabilities times s_v are rounded to bf16 for the product with vc (fp32 accumulation),
+ *   o is rounded to bf16. A row that sees no key gives zeros. What lies in slots a row does
+ *   not see (uninitialised codes, infinite or NaN scales) has no effect on it.
+ *   max_q: the largest number of new tokens of a sequence, or a bound on it. It chooses the
+ *     kernels only; a wrong one costs time, never results.
+ *   scale: finite and >= 0, usually fp32(1/sqrt(D)). window, sinks >= 0.
+ *   ws: sdnq_attention_paged_workspace(H, Hkv, D) bytes, 256-byte aligned, for partial sums of
+ *     one call; nothing in it needs clearing or is kept between calls. Calls that may overlap
+ *     on the GPU need separate ones.
+ *   out [T][H][D] bf16, token stride ldo; rows past cu_q[B] (past B without cu_q) are left as
+ *     they are. out may not overlap q.
+ * A page id out of range hides its keys; row offsets that decrease or leave [0, T] leave their
+ * sequence out; a length below 0 or above max_pages * page counts as that bound. Each records
+ * SDNQ_ERR_INDEX. T == 0 or B == 0 is a no-op.
+ */
+int64_t sdnq_attention_paged_workspace(int64_t H, int64_t Hkv, int64_t D);
+sdnq_status sdnq_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,
+                                 const int32_t *cu_q, const int32_t *lens, int64_t B,
+                                 const int32_t *table, int64_t max_pages, int64_t ldt,
+                                 const int8_t *codes, const float *scales, int64_t pages, int32_t page, int64_t Hkv,
+                                 int64_t D, int64_t max_q, int32_t group, float scale,
+                                 int64_t window, int64_t sinks, void *ws, int64_t ws_bytes,
+                                 uint16_t *out, int64_t ldo, void *stream);
+
+/*
  * GELU between the up and down projections of a DiT MLP (exact erf form,
  * x * Phi(x), rounded once to bf16). Not on the pages; the MLP workload needs it.
  *   in [M, N] bf16 row stride ld_in; out [M, N] bf16 row stride ld_out (may alias in when
@@ -359,8 +436,9 @@ sdnq_status sdnq_gelu_bf16(const uint16_t *in, int64_t M, int64_t N, int64_t ld_
 
 /*
  * Synchronises `stream`, then reads and clears the device error word that bounded waits
- * inside the kernels set when they give up. Returns SDNQ_OK, SDNQ_ERR_TIMEOUT, or
- * SDNQ_ERR_CUDA if the synchronisation itself failed.
+ * inside the kernels set when they give up, and that the calls on a paged cache set when a
+ * slot, page id, length or row offset is out of range. Returns SDNQ_OK, SDNQ_ERR_TIMEOUT,
+ * SDNQ_ERR_INDEX, or SDNQ_ERR_CUDA if the synchronisation itself failed.
  */
 sdnq_status sdnq_device_status(void *stream);
 
