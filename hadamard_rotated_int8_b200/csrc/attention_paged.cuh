@@ -36,6 +36,11 @@ struct PagedParams {
     int32_t group;           // min(group, D)
     float scale;
     float c_g;
+    int32_t rows_min, rows_max;   // sequences of rows_min < (token, head) rows a kv head <= rows_max
+    int32_t least_tiles;     // a block's share of the tile list is at least this
+    float *partial;          // workspace: pieces, and what the blocks say of them
+    void *desc;
+    uint64_t timeout_ns;
 };
 
 // A sequence as the device arrays give it, made safe: rows [q0, q0 + n) lie in [0, T), the
@@ -117,95 +122,811 @@ __device__ __forceinline__ uint32_t warp_quant_row(float (&v)[E], int32_t g, flo
     return w;
 }
 
-// One warp per (query row, head); a lane holds D / 32 elements of the row, and one key's dot
-// product is reduced by shuffles.
+// ---------------------------------------------------------------- work split
+//
+// A segment is one (sequence, kv head, tile of query rows); the rows of a tile are (token,
+// head of the kv head's share) pairs in that order, so grouped heads share the keys and values
+// they read. A segment's keys are walked in tiles: those of the sinks, then those from the
+// first row's window to the last row's position. All tiles of all segments form one list
+// (sequence, then kv head, then query tile), and block c takes the equal share
+// [c * per, (c + 1) * per) of it, whatever segments that meets: the blocks finish together for
+// any mix of lengths. A segment that one block has whole is written out by it; of the others,
+// each block leaves its unnormalised sums, and a second kernel joins them in list order (so
+// the results do not depend on timing).
+
+struct PagedTiles {
+    int32_t nt;       // key tiles of the segment
+    int32_t ns, w0;   // tiles 0..ns-1 hold the sinks, the others start at tile w0
+};
+
+// Query tiles of a sequence; 0: the sequence is not this kernel's.
+template <int ROWS>
+__device__ __forceinline__ int32_t paged_qtiles(const PagedParams &p, const PagedSeq &s)
+{
+    const int32_t rows = s.n * p.share;
+    return rows > p.rows_min && rows <= p.rows_max ? (rows - 1) / ROWS + 1 : 0;
+}
+
+// The key tiles of TILE keys of query tile q (ROWS rows).
+template <int TILE, int ROWS>
+__device__ __forceinline__ PagedTiles paged_tiles(const PagedParams &p, int32_t n, int32_t len, int32_t q)
+{
+    const int32_t first = q * ROWS / p.share, last = min(q * ROWS + ROWS - 1, n * p.share - 1) / p.share;
+    const int32_t end = max(len - n + last + 1, 0);   // keys [0, end) are in reach
+    const int32_t low = p.window > 0 ? max(0, len - n + first - p.window + 1) : 0;
+    PagedTiles t;
+    t.w0 = low / TILE;
+    t.ns = min((min(p.sinks, end) + TILE - 1) / TILE, t.w0);
+    t.nt = max(t.ns + (end + TILE - 1) / TILE - t.w0, 1);
+    return t;
+}
+
+// Where a block is in the list of tiles.
+struct PagedWalk {
+    int32_t b, kvh, q, i;   // sequence, kv head, query tile, key tile of the segment
+    int32_t qt;             // query tiles of the sequence
+    PagedSeq s;
+    PagedTiles t;
+};
+
+template <int TILE, int ROWS>
+__device__ __forceinline__ void walk_next_segment(const PagedParams &p, PagedWalk &w)
+{
+    w.i = 0;
+    if (++w.q == w.qt) {
+        w.q = 0;
+        if (++w.kvh == p.Hkv) {
+            w.kvh = 0;
+            do {
+                if (++w.b >= p.B)
+                    return;
+                w.s = paged_seq(p, w.b);
+                w.qt = paged_qtiles<ROWS>(p, w.s);
+            } while (w.qt == 0);
+        }
+    }
+    w.t = paged_tiles<TILE, ROWS>(p, w.s.n, w.s.len, w.q);
+}
+
+__device__ __forceinline__ int64_t warp_inclusive_sum(int64_t v, uint32_t lane)
+{
+#pragma unroll
+    for (uint32_t x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
+        if (lane >= x)
+            v += o;
+    }
+    return v;
+}
+
+// The tiles of the 32 sequences b (one a lane): a sequence of up to 2 query tiles is its
+// lane's work, longer ones are walked by the whole warp.
+template <int TILE, int ROWS>
+__device__ __forceinline__ int64_t sequence_tiles(const PagedParams &p, int32_t b, uint32_t lane, PagedSeq &s,
+                                                  int32_t &qt)
+{
+    s.q0 = 0, s.n = 0, s.len = 0, qt = 0;
+    if (b < p.B) {
+        s = paged_seq(p, b);
+        qt = paged_qtiles<ROWS>(p, s);
+    }
+    int64_t sum = 0;
+    for (int32_t q = 0; q < min(qt, 2); ++q)
+        sum += paged_tiles<TILE, ROWS>(p, s.n, s.len, q).nt;
+    for (uint32_t big = __ballot_sync(0xffffffffu, qt > 2); big != 0u; big &= big - 1u) {
+        const int src = __ffs(static_cast<int>(big)) - 1;
+        const int32_t n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
+        const int32_t qn = __shfl_sync(0xffffffffu, qt, src);
+        int64_t part = 0;
+        for (int32_t q = 2 + static_cast<int32_t>(lane); q < qn; q += 32)
+            part += paged_tiles<TILE, ROWS>(p, n, len, q).nt;
+        part = __shfl_sync(0xffffffffu, warp_inclusive_sum(part, lane), 31);
+        if (static_cast<int>(lane) == src)
+            sum += part;
+    }
+    return sum * p.Hkv;
+}
+
+// Counts the list's tiles (the whole block), and finds where share blockIdx.x of `blocks`
+// begins: tile `first` of `total`, shares of `per` >= `least` tiles. `found`: 4 words of shared
+// memory.
+template <int TILE, int ROWS, int THREADS>
+__device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks, int32_t least, int32_t *found,
+                                           int64_t &first, int64_t &per, int64_t &total, PagedWalk &w)
+{
+    constexpr int WARPS = THREADS / 32;
+    __shared__ int64_t warp_sum[WARPS];
+    const uint32_t lane = lane_id();
+    const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5);
+    const int32_t groups = (p.B + 31) / 32, each = (groups + WARPS - 1) / WARPS;
+    const int32_t g0 = min(warp * each, groups), g1 = min(g0 + each, groups);
+    PagedSeq s;
+    int32_t qt;
+    int64_t sum = 0;
+    for (int32_t g = g0; g < g1; ++g)
+        sum += sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
+    sum = __shfl_sync(0xffffffffu, warp_inclusive_sum(sum, lane), 31);
+    if (lane == 0)
+        warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        if (i < warp)
+            before += warp_sum[i];
+        total += warp_sum[i];
+    }
+    per = (total + blocks - 1) / blocks;
+    per = per < least ? least : per;
+    first = static_cast<int64_t>(blockIdx.x) * per;
+    if (first < total && first >= before && first < before + sum) {   // one warp
+        int64_t rest = first - before;
+        for (int32_t g = g0; g < g1; ++g) {
+            const int64_t mine = sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
+            const int64_t incl = warp_inclusive_sum(mine, lane);
+            const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+            if (rest >= all) {
+                rest -= all;
+                continue;
+            }
+            const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, rest < incl))) - 1;
+            const int32_t n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
+            const int32_t qn = __shfl_sync(0xffffffffu, qt, src);
+            const int64_t head = __shfl_sync(0xffffffffu, mine, src) / p.Hkv;
+            rest -= __shfl_sync(0xffffffffu, incl - mine, src);
+            const int64_t kvh = rest / head;
+            rest -= kvh * head;
+            for (int32_t q0 = 0; q0 < qn; q0 += 32) {
+                const int32_t q = q0 + static_cast<int32_t>(lane);
+                const int64_t nt = q < qn ? paged_tiles<TILE, ROWS>(p, n, len, q).nt : 0;
+                const int64_t qi = warp_inclusive_sum(nt, lane);
+                const int64_t qall = __shfl_sync(0xffffffffu, qi, 31);
+                if (rest >= qall) {
+                    rest -= qall;
+                    continue;
+                }
+                const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, rest < qi))) - 1;
+                rest -= __shfl_sync(0xffffffffu, qi - nt, at);
+                if (lane == 0) {
+                    found[0] = g * 32 + src;
+                    found[1] = static_cast<int32_t>(kvh);
+                    found[2] = q0 + at;
+                    found[3] = static_cast<int32_t>(rest);
+                }
+                break;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+    w.b = 0, w.kvh = 0, w.q = 0, w.i = 0, w.qt = 0;
+    if (first < total) {
+        w.b = found[0], w.kvh = found[1], w.q = found[2], w.i = found[3];
+        w.s = paged_seq(p, w.b);
+        w.qt = paged_qtiles<ROWS>(p, w.s);
+        w.t = paged_tiles<TILE, ROWS>(p, w.s.n, w.s.len, w.q);
+    }
+}
+
+// ---------------------------------------------------------------- few query rows
+//
+// Decoding: up to 16 query rows share a kv head, every key and value byte is used once, and
+// the kernel is bound by reading them. Per key and kv head 2 (D + 4) bytes arrive; at the
+// copy rate of the chip an SM gets about 24 bytes a cycle, so a key of D = 128 may take about
+// 11 cycles. The small matrix instructions (mma.sync) keep up with that easily at 16 rows,
+// and their register operands allow each warp to work alone:
+// - a producer warp streams tiles of 64 keys through a ring of 4 stages (one box of the page
+//   holds keys and values; 64-key pages make one copy of 16 KB), across segment borders, so the
+//   ring stays full while a segment is being finished;
+// - 4 warps take 16 keys of each tile each, with their own running maximum, sum and output
+//   (16 x D fp32 in registers): S = q k^T in int8 (m16n8k32), the exponentials, and
+//   O += (p s_v) v with v's codes turned into bf16 in registers (m16n8k16). They meet only at
+//   the end of a segment.
+// Two blocks per SM keep up to 132 KB in flight.
+//
+// Fragments. The key of column n of an 8-key block is PI(n), PI(2t) = 2t + (t >> 1) and
+// PI(2t + 1) = PI(2t) ^ 4, which makes both the keys' 16-byte loads (two keys' rows per
+// quarter warp) and the values' (four keys' rows) free of bank conflicts in the 128-byte
+// swizzle. A lane's value column n of block j is dim (D / 8) n + j, its key bytes are 16-byte
+// chunks: any order of the contracted index serves as long as both operands follow it.
+
+constexpr int kFewTile = 64;      // keys per stage
+constexpr int kFewRows = 16;      // query rows of a tile
+constexpr int kFewStages = 4;
+constexpr int kFewThreads = 160;  // 4 warps and the producer
+constexpr int kPagedMaxSms = 160; // the workspace's size assumes no more
+constexpr int kFewPerSm = 2;
+
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p)
+struct FewConfig {
+    static constexpr int STAGE = 2 * kFewTile * D;              // codes of a stage
+    static constexpr int SC_OFF = kFewStages * STAGE;           // scales: 2 * 64 fp32 a stage
+    static constexpr int O_OFF = SC_OFF + kFewStages * 2 * kFewTile * 4;
+    static constexpr int O_LD = D + 4;                          // floats
+    static constexpr int Q_OFF = O_OFF + 4 * kFewRows * O_LD * 4;
+    static constexpr int QS_OFF = Q_OFF + kFewRows * D;
+    static constexpr int ML_OFF = QS_OFF + kFewRows * 4;        // [4 warps][16 rows] (m, l)
+    static constexpr int BAR_OFF = ML_OFF + 4 * kFewRows * 8;
+    static constexpr int META_OFF = BAR_OFF + 2 * kFewStages * 8;   // valid pages of each stage
+    static constexpr int SCAN_OFF = META_OFF + kFewStages * 4;
+    static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 64;
+    static_assert(BAR_OFF % 8 == 0 && kFewPerSm * (SMEM_BYTES + 1024) <= 228 * 1024,
+                  "shared memory per SM");
+};
+
+// Workspace: a piece's sums [16][D], then its (m, l) [16][2]; two pieces a block (0: of the
+// segment that began before the block, 1: of the one that goes on behind it).
+template <int D>
+__host__ __device__ constexpr int64_t few_piece_floats() { return kFewRows * (D + 2); }
+
+struct FewDesc {       // the segment that begins in a block and goes on behind it
+    int32_t pieces;    // 0: none
+    int32_t q0, rows;  // first query row of the sequence, valid rows of the tile
+    int32_t head0;     // first head of the share
+    int32_t r0;        // first (token, head) row of the tile
+};
+
+__device__ __forceinline__ void mma_m16n8k32_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+                 " {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_m16n8k16_bf16(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                  uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3},"
+                 " {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte `j` of a and of b, two int8 codes, as a bf16 pair (a low), exactly. With m the low 7
+// bits and s the sign bit of a code, its value is (128 + m) - (128 or 256 by s); 0x4300 | m and
+// 0x4300 | (s << 7) are the bf16 patterns of the two.
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t a, uint32_t b, int j)
+{
+    const uint32_t pick = static_cast<uint32_t>(j) * 0x1111u + 0x4400u;
+    const uint32_t t = __byte_perm(a, b, pick);   // bytes a_j, a_j, b_j, b_j; 0 and 2 are used
+    uint32_t hi = (t & 0x007f007fu) | 0x43004300u, lo = (t & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&hi),
+                                     *reinterpret_cast<__nv_bfloat162 *>(&lo));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float lds_f(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Barrier of the four warps that compute.
+__device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// One output row held by a warp (lane l has D / 32 elements): un-rotated, divided, stored.
+// l == 0: the row saw no key.
+template <int D>
+__device__ __forceinline__ void paged_store_row(const PagedParams &p, float (&v)[D / 32], float l,
+                                                int64_t t, int32_t head, uint32_t lane)
 {
     constexpr int E = D / 32;
-    grid_dependency_wait();
-    const uint32_t lane = lane_id();
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (w >= static_cast<int64_t>(p.T) * p.H)
-        return;
-    const int32_t t = static_cast<int32_t>(w / p.H), h = static_cast<int32_t>(w - static_cast<int64_t>(t) * p.H);
-    int32_t b = t;
-    if (p.cu != nullptr) {   // the last sequence that starts at or before row t
-        int32_t lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (p.cu[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        b = lo;
+    warp_butterfly(v, p.group, lane);
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(p.c_g, l);
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * i] * inv, v[2 * i + 1] * inv);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h2);
     }
-    if (b >= p.B)
-        return;
-    const PagedSeq sq = paged_seq(p, b);
-    if (t < sq.q0 || t >= sq.q0 + sq.n)
-        return;
-    const int32_t pos = sq.len - sq.n + (t - sq.q0);
-    float v[E];
-    const uint16_t *qr = p.q + static_cast<int64_t>(t) * p.ldq + static_cast<int64_t>(h) * D + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        v[i] = __uint_as_float(static_cast<uint32_t>(qr[i]) << 16);
-    float s;
-    const uint32_t qw = warp_quant_row<E>(v, p.group, p.c_g, lane, s);
-    const float f = s * p.scale * 1.4426950408889634f;
-    float m = -INFINITY, l = 0.0f, acc[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        acc[i] = 0.0f;
-    const int32_t kvh = h / p.share;
-    const int32_t low = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    for (int32_t j = 0; j <= pos; ++j) {
-        if (j < low && j >= p.sinks)
-            j = low;
-        const int32_t id = p.table[static_cast<int64_t>(b) * p.table_ld + (j >> p.page_shift)];
-        if (id < 0 || id >= p.pages) {
-            if (lane == 0)
-                atomicOr(&g_device_error, kDevIndex);
-            continue;
+    uint16_t *o = p.o + t * p.ldo + static_cast<int64_t>(head) * D + lane * E;
+    if (E == 4)
+        st_v2(o, w[0], w[E / 2 - 1]);
+    else
+        *reinterpret_cast<uint32_t *>(o) = w[0];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, kFewPerSm)
+    attn_few_kernel(const __grid_constant__ CUtensorMap tmPool, const PagedParams p)
+{
+    using C = FewConfig<D>;
+    constexpr int NST = kFewStages, E = D / 32, H2 = D / 64, DB = D / 8;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_addr);
+    __shared__ int abort_flag;
+    volatile int *abort = &abort_flag;
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+    auto full = [&](int s) { return base + C::BAR_OFF + 8u * s; };
+    auto empty = [&](int s) { return base + C::BAR_OFF + 8u * (NST + s); };
+    volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 4);
         }
-        const int64_t krow = (((static_cast<int64_t>(id) * p.Hkv + kvh) * 2) << p.page_shift) +
-                             (j & ((1 << p.page_shift) - 1));
-        const int64_t vrow = krow + (1ll << p.page_shift);
-        uint32_t kw, vw;
-        if (E == 4) {
-            kw = *reinterpret_cast<const uint32_t *>(p.codes + krow * D + lane * E);
-            vw = *reinterpret_cast<const uint32_t *>(p.codes + vrow * D + lane * E);
-        } else {
-            kw = *reinterpret_cast<const uint16_t *>(p.codes + krow * D + lane * E);
-            vw = *reinterpret_cast<const uint16_t *>(p.codes + vrow * D + lane * E);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmPool);
+    }
+    grid_dependents_launch();
+    grid_dependency_wait();
+
+    int64_t first, per, total;
+    PagedWalk w;
+    find_share<kFewTile, kFewRows, kFewThreads>(p, gridDim.x, p.least_tiles, reinterpret_cast<int32_t *>(smem + C::SCAN_OFF),
+                                                first, per, total, w);   // also: barriers initialised
+    FewDesc *desc = reinterpret_cast<FewDesc *>(p.desc) + blockIdx.x;
+    if (first >= total) {
+        if (threadIdx.x == 0)
+            desc->pieces = 0;
+        return;
+    }
+    const int64_t last = min(first + per, total);
+    const int64_t count = last - first;
+    const int32_t pp = min(1 << p.page_shift, kFewTile);        // keys of a page in a tile
+    const int32_t pp_shift = min(p.page_shift, 6);
+    const int32_t nchunk = kFewTile >> pp_shift;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        const int32_t tile_shift = 6 - p.page_shift;            // < 0: several tiles a page
+        int64_t n = 0;
+        bool ok = true;
+        while (ok && n < count) {
+            const int32_t kvh = w.kvh;
+            const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
+            const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
+            // Page ids are read 32 at a time, a batch ahead of their use; entry e is chunk
+            // e % nchunk of the piece's tile e / nchunk.
+            auto fetch = [&](int32_t e0) {
+                const int32_t e = e0 + static_cast<int32_t>(lane);
+                const int32_t i = w.i + e / nchunk;
+                if (i >= w.i + tiles)
+                    return -1;
+                const int32_t tile = i < w.t.ns ? i : w.t.w0 + i - w.t.ns;
+                const int32_t j = tile * kFewTile + (e % nchunk) * pp;
+                if (j >= w.s.len)
+                    return -1;
+                const int32_t id = row[tile_shift >= 0 ? j >> p.page_shift : tile >> -tile_shift];
+                if (id < 0 || id >= p.pages) {
+                    atomicOr(&g_device_error, kDevIndex);
+                    return -1;
+                }
+                return id;
+            };
+            int32_t ids = fetch(0), ids_next = fetch(32), e0 = 0;
+            for (int32_t k = 0; k < tiles; ++k, ++n) {
+                const int st = static_cast<int>(n % NST);
+                if (k * nchunk >= e0 + 32) {
+                    ids = ids_next;
+                    e0 += 32;
+                    ids_next = fetch(e0 + 32);
+                }
+                // lane c < nchunk has page chunk c of this tile
+                const int32_t id = __shfl_sync(0xffffffffu, ids, (k * nchunk - e0 + static_cast<int32_t>(lane)) & 31);
+                const bool mine = static_cast<int32_t>(lane) < nchunk && id >= 0;
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine);
+                bool got = true;
+                if (lane == 0)
+                    got = mbar_wait_bounded(empty(st), (static_cast<uint32_t>(n / NST) & 1u) ^ 1u, abort,
+                                            p.timeout_ns);
+                if (!__shfl_sync(0xffffffffu, static_cast<int>(got), 0)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    meta[st] = valid;
+                    mbar_arrive_expect_tx(full(st), static_cast<uint32_t>(__popc(valid)) * 2u * pp * (D + 4));
+                }
+                __syncwarp();
+                if (mine) {
+                    const int32_t i = w.i + k;
+                    const int32_t tile = i < w.t.ns ? i : w.t.w0 + i - w.t.ns;
+                    const int32_t prow = static_cast<int32_t>(((static_cast<int64_t>(id) * p.Hkv + kvh) * 2) << p.page_shift);
+                    const uint32_t dst = base + st * C::STAGE + lane * 2u * pp * D;
+                    const uint32_t sdst = base + C::SC_OFF + (st * 2 * kFewTile + lane * 2 * pp) * 4;
+                    if (tile_shift >= 0) {     // the chunk is the page: its keys, then its values
+                        tma_load_2d(dst, &tmPool, full(st), 0, prow);
+                        bulk_load_1d(sdst, p.scales + prow, 8u * pp, full(st));
+                    } else {
+                        const int32_t off = (tile * kFewTile) & ((1 << p.page_shift) - 1);
+                        const int32_t vrow = prow + (1 << p.page_shift);
+                        tma_load_2d(dst, &tmPool, full(st), 0, prow + off);
+                        tma_load_2d(dst + kFewTile * D, &tmPool, full(st), 0, vrow + off);
+                        bulk_load_1d(sdst, p.scales + prow + off, 4u * pp, full(st));
+                        bulk_load_1d(sdst + 4 * pp, p.scales + vrow + off, 4u * pp, full(st));
+                    }
+                }
+            }
+            walk_next_segment<kFewTile, kFewRows>(p, w);
         }
-        int32_t dot = __dp4a(static_cast<int>(qw), static_cast<int>(kw), 0);
-        dot = __reduce_add_sync(0xffffffffu, dot);
-        const float y = static_cast<float>(dot) * p.scales[krow] * f;
-        if (y > m) {
-            const float a = ex2_approx(m - y);
-            l *= a;
+        // every copy has landed before the block may end (its consumers may have given up)
+        if (lane == 0) {
+            volatile int no_abort = 0;
+            for (int64_t j = n - NST < 0 ? 0 : n - NST; j < n; ++j)
+                mbar_wait_bounded(full(static_cast<int>(j % NST)), static_cast<uint32_t>(j / NST) & 1u, &no_abort,
+                                  p.timeout_ns);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- the four warps
+    const uint32_t g = lane >> 2, t = lane & 3u;
+    const uint32_t e = 2u * t + (t >> 1);                         // PI(2t)
+    const uint32_t krow_n = (2u * (g >> 1) + (g >> 2)) ^ ((g & 1u) << 2);   // PI(g)
+    const int32_t my_key = static_cast<int32_t>(warp) * 16;
+    const uint32_t my_chunk = static_cast<uint32_t>(my_key >> pp_shift);
+    const uint32_t my_krow = my_chunk * 2u * pp + (my_key & (pp - 1));
+    float *obuf = reinterpret_cast<float *>(smem + C::O_OFF);
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
+    float *qs = reinterpret_cast<float *>(smem + C::QS_OFF);
+    bool ok = true;
+    int64_t n = 0;
+    int piece_no = 0;
+    while (n < count) {
+        const int32_t r0 = w.q * kFewRows, head0 = w.kvh * p.share;
+        const int32_t rows = min(kFewRows, w.s.n * p.share - r0);
+        const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
+        // this warp's four query rows: codes and scales
+#pragma unroll 1
+        for (int rr = 0; rr < 4; ++rr) {
+            const int32_t lr = static_cast<int32_t>(warp) * 4 + rr, r = r0 + lr;
+            float v[E];
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                acc[i] *= a;
-            m = y;
+                v[i] = 0.0f;
+            if (lr < rows) {
+                const int32_t ti = r / p.share;
+                const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + ti) * p.ldq +
+                                    static_cast<int64_t>(head0 + r - ti * p.share) * D + lane * E;
+                uint32_t x[E / 2];
+                if (E == 4) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(q);
+                    x[0] = a.x, x[E / 2 - 1] = a.y;
+                } else {
+                    x[0] = *reinterpret_cast<const uint32_t *>(q);
+                }
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    v[2 * i] = __uint_as_float(x[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+                }
+            }
+            float sq;
+            const uint32_t c = warp_quant_row<E>(v, p.group, p.c_g, lane, sq);
+            if (E == 4)
+                *reinterpret_cast<uint32_t *>(smem + C::Q_OFF + lr * D + lane * E) = c;
+            else
+                *reinterpret_cast<uint16_t *>(smem + C::Q_OFF + lr * D + lane * E) = static_cast<uint16_t>(c);
+            if (lane == 0)
+                qs[lr] = sq;
         }
-        const float e = ex2_approx(y - m);
-        l += e;
-        const float ev = e * p.scales[vrow];
+        few_sync();
+        uint4 qa[2][H2];     // rows g and g + 8, 16-byte chunk t of each 64-element half
+        float row_f[2];
+        int32_t pos[2], low[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t lr = static_cast<int32_t>(g) + 8 * u;
+#pragma unroll
+            for (int h = 0; h < H2; ++h)
+                qa[u][h] = lds_u4(base + C::Q_OFF + lr * D + h * 64 + t * 16);
+            // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out (attention.cuh)
+            row_f[u] = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
+            pos[u] = w.s.len - w.s.n + (r0 + min(lr, rows - 1)) / p.share;
+            low[u] = p.window > 0 ? pos[u] - p.window + 1 : INT32_MIN;
+        }
+        const int32_t pos_first = w.s.len - w.s.n + r0 / p.share;
+        const int32_t pos_last = w.s.len - w.s.n + (r0 + rows - 1) / p.share;
+        const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : INT32_MIN;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float o[DB][4];
+#pragma unroll
+        for (int j = 0; j < DB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[j][i] = 0.0f;
+
+#pragma unroll 1
+        for (int32_t k = 0; k < tiles; ++k, ++n) {
+            const int st = static_cast<int>(n % NST);
+            const int32_t ti = w.i + k;
+            const int32_t j0 = (ti < w.t.ns ? ti : w.t.w0 + ti - w.t.ns) * kFewTile + my_key;
+            const bool got = ok && mbar_wait_bounded(full(st), static_cast<uint32_t>(n / NST) & 1u, abort,
+                                                     p.timeout_ns);
+            ok = __all_sync(0xffffffffu, got);
+            if (ok) {
+                const bool there = ((meta[st] >> my_chunk) & 1u) != 0u;
+                // nothing of these 16 keys is visible to any row: leave them
+                const bool some = there && j0 <= pos_last &&
+                                  (j0 + 15 >= (p.window > 0 ? pos_first - p.window + 1 : INT32_MIN) ||
+                                   j0 < p.sinks);
+                if (some) {
+                    const uint32_t codes = base + st * C::STAGE + my_krow * D;
+                    const uint32_t sc = base + C::SC_OFF + (st * 2 * kFewTile + my_krow) * 4;
+                    int32_t acc[2][4];
+                    uint4 kb[2][H2];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int h = 0; h < H2; ++h) {
+                            const uint32_t sw = D == 128 ? (t + 4u * h) ^ krow_n : t ^ (krow_n >> 1);
+                            kb[nb][h] = lds_u4(codes + (8u * nb + krow_n) * D + sw * 16u);
+                        }
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[nb][i] = 0;
+#pragma unroll
+                        for (int h = 0; h < H2; ++h) {
+                            mma_m16n8k32_s8(acc[nb], qa[0][h].x, qa[1][h].x, qa[0][h].y, qa[1][h].y,
+                                            kb[nb][h].x, kb[nb][h].y);
+                            mma_m16n8k32_s8(acc[nb], qa[0][h].z, qa[1][h].z, qa[0][h].w, qa[1][h].w,
+                                            kb[nb][h].z, kb[nb][h].w);
+                        }
+                    }
+                    // acc[nb][2u + c]: row g + 8u, key 8 nb + PI(2t + c)
+                    float sk[2][2], sv[2][2], y[2][4];
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t a = sc + (8u * nb + (c ? e ^ 4u : e)) * 4u;
+                            sk[nb][c] = lds_f(a);
+                            sv[nb][c] = lds_f(a + 4u * pp);
+                        }
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[nb][i] = static_cast<float>(acc[nb][i]) * sk[nb][i & 1];
+                    const bool whole = j0 + 15 <= pos_first && (j0 >= low_last || j0 + 16 <= p.sinks);
+                    uint32_t hidden = 0u;
+                    if (!whole) {
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int32_t j = j0 + 8 * nb + static_cast<int32_t>((i & 1) ? e ^ 4u : e);
+                                const bool see = j <= pos[i >> 1] && (j >= low[i >> 1] || j < p.sinks);
+                                if (!see) {
+                                    y[nb][i] = -INFINITY;
+                                    hidden |= 1u << (nb * 4 + i);
+                                }
+                            }
+                    }
+                    float alpha[2];
+                    bool grew = false;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float mx = fmaxf(fmaxf(y[0][2 * u], y[0][2 * u + 1]), fmaxf(y[1][2 * u], y[1][2 * u + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float mb = mx * row_f[u];
+                        // the sums are rescaled only when the maximum grows by more than 2^8
+                        const bool grow = mb > m[u] + 8.0f;
+                        alpha[u] = grow ? ex2_approx(m[u] - mb) : 1.0f;
+                        m[u] = grow ? mb : m[u];
+                        grew |= grow;
+                    }
+                    if (__any_sync(0xffffffffu, grew)) {
+                        l[0] *= alpha[0];
+                        l[1] *= alpha[1];
+#pragma unroll
+                        for (int j = 0; j < DB; ++j) {
+                            mul2(o[j][0], o[j][1], o[j][0], o[j][1], alpha[0], alpha[0]);
+                            mul2(o[j][2], o[j][3], o[j][2], o[j][3], alpha[1], alpha[1]);
+                        }
+                    }
+                    uint32_t pa[2][2];   // [nb][u]: probabilities times s_v, a bf16 pair
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float neg_m = m[u] == -INFINITY ? 0.0f : -m[u];
+#pragma unroll
+                        for (int nb = 0; nb < 2; ++nb) {
+                            float pr[2];
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float x = ex2_approx(__fmaf_rn(y[nb][2 * u + c], row_f[u], neg_m));
+                                l[u] += x;
+                                // a hidden key adds 0 whatever its scale holds
+                                pr[c] = (hidden >> (nb * 4 + 2 * u + c)) & 1u ? 0.0f : x * sv[nb][c];
+                            }
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
+                            pa[nb][u] = *reinterpret_cast<const uint32_t *>(&h2);
+                        }
+                    }
+                    // values of keys PI(2t), PI(2t+1) of both 8-key blocks, this lane's DB dims
+                    uint32_t vb[4][DB / 4];
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t kr = (kk & 1) ? e ^ 4u : e;
+                        const uint32_t row = codes + (pp + 8u * (kk >> 1) + kr) * D;
+                        if (D == 128) {
+                            const uint4 a = lds_u4(row + ((g ^ kr) << 4));
+                            vb[kk][0] = a.x, vb[kk][1] = a.y, vb[kk][DB / 4 - 2] = a.z, vb[kk][DB / 4 - 1] = a.w;
+                        } else {
+                            const uint32_t a = row + (((g >> 1) ^ (kr >> 1)) << 4) + (g & 1u) * 8u;
+                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                         : "=r"(vb[kk][0]), "=r"(vb[kk][1]) : "r"(a) : "memory");
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < DB; ++j) {
+                        const uint32_t b0 = codes_to_bf16x2(vb[0][j >> 2], vb[1][j >> 2], j & 3);
+                        const uint32_t b1 = codes_to_bf16x2(vb[2][j >> 2], vb[3][j >> 2], j & 3);
+                        mma_m16n8k16_bf16(o[j], pa[0][0], pa[0][1], pa[1][0], pa[1][1], b0, b1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty(st));
+        }
+
+        // ------------------------------------------------ join the four warps' sums
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
+            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
+            if (t == 0)
+                ml[warp * kFewRows + g + 8 * u] = make_float2(m[u], l[u]);
+        }
+        // lane (g, t): dims [2 DB t, 2 DB (t + 1)) of rows g and g + 8: o[j][0] is dim 2 DB t + j,
+        // o[j][1] dim 2 DB t + DB + j
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < 2 * DB / 4; ++c) {
+                float4 x;
+                const int hb = c / (DB / 4), jj = (c % (DB / 4)) * 4;
+                x.x = o[jj][2 * u + hb], x.y = o[jj + 1][2 * u + hb], x.z = o[jj + 2][2 * u + hb],
+                x.w = o[jj + 3][2 * u + hb];
+                *reinterpret_cast<float4 *>(obuf + (warp * kFewRows + g + 8 * u) * C::O_LD + 2 * DB * t +
+                                            4 * c) = x;
+            }
+        few_sync();
+        const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
+        float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * few_piece_floats<D>();
+#pragma unroll 1
+        for (int rr = 0; rr < 4; ++rr) {
+            const int32_t lr = static_cast<int32_t>(warp) * 4 + rr;
+            if (lr >= rows)
+                break;
+            float2 x[4];
+            float mm = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = ml[i * kFewRows + lr];
+                mm = fmaxf(mm, x[i].x);
+            }
+            float ll = 0.0f, v[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = x[i].x == -INFINITY ? 0.0f : ex2_approx(x[i].x - mm);
+                ll = __fmaf_rn(x[i].y, f, ll);
+                const float *src = obuf + (i * kFewRows + lr) * C::O_LD + lane * E;
+#pragma unroll
+                for (int d = 0; d < E; ++d)
+                    v[d] = __fmaf_rn(src[d], f, v[d]);
+            }
+            const int32_t r = r0 + lr, tok = r / p.share;
+            if (begins && ends) {
+                if (ok)
+                    paged_store_row<D>(p, v, ll, w.s.q0 + tok, head0 + r - tok * p.share, lane);
+            } else {
+#pragma unroll
+                for (int d = 0; d < E; ++d)
+                    ws[lr * D + lane * E + d] = v[d];
+                if (lane == 0)
+                    *reinterpret_cast<float2 *>(ws + kFewRows * D + 2 * lr) = make_float2(mm, ll);
+            }
+        }
+        if (threadIdx.x == 0 && begins && !ends) {
+            // the segment's last tile is nt - tiles further on: that many blocks hold pieces
+            const int64_t end = first + n - tiles + w.t.nt - 1;
+            desc->pieces = static_cast<int32_t>(end / per) - static_cast<int32_t>(blockIdx.x) + 1;
+            desc->q0 = w.s.q0;
+            desc->rows = rows;
+            desc->head0 = head0;
+            desc->r0 = r0;
+            piece_no = 1;
+        }
+        walk_next_segment<kFewTile, kFewRows>(p, w);
+        few_sync();   // obuf, ml and the query codes are free again
+    }
+    if (threadIdx.x == 0 && piece_no == 0)
+        desc->pieces = 0;
+}
+
+// Joins the pieces of the segments that several blocks share: block (c, y) takes rows y, y +
+// gridDim.y, ... of the segment that begins in block c. Eight warps take the pieces in turn.
+constexpr int kJoinThreads = 256;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedParams p)
+{
+    constexpr int E = D / 32, W = kJoinThreads / 32;
+    constexpr int64_t PIECE = ROWS * (D + 2);
+    __shared__ float part[W][D];
+    __shared__ float2 part_ml[W];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const FewDesc d = reinterpret_cast<const FewDesc *>(p.desc)[blockIdx.x];
+    const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5);
+    const uint32_t lane = lane_id();
+    if (d.pieces == 0)
+        return;
+    for (int32_t lr = blockIdx.y; lr < d.rows; lr += static_cast<int32_t>(gridDim.y)) {
+        float m = -INFINITY, l = 0.0f, v[E];
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            acc[i] = __fmaf_rn(ev, static_cast<float>(static_cast<int8_t>(vw >> (8 * i))), acc[i]);
-    }
-    warp_butterfly(acc, p.group, lane);
-    const float inv = l > 0.0f ? p.c_g / l : 0.0f;
-    uint16_t *orow = p.o + static_cast<int64_t>(t) * p.ldo + static_cast<int64_t>(h) * D + lane * E;
+            v[i] = 0.0f;
+#pragma unroll 4
+        for (int32_t k = warp; k < d.pieces; k += W) {
+            const float *ws = p.partial + ((static_cast<int64_t>(blockIdx.x) + k) * 2 + (k == 0 ? 1 : 0)) * PIECE;
+            const float2 x = *reinterpret_cast<const float2 *>(ws + ROWS * D + 2 * lr);
+            float a[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const __nv_bfloat16 r = __float2bfloat16_rn(l > 0.0f ? acc[i] * inv : 0.0f);
-        orow[i] = *reinterpret_cast<const uint16_t *>(&r);
+            for (int i = 0; i < E; ++i)
+                a[i] = ws[lr * D + lane * E + i];
+            const float mn = fmaxf(m, x.x);
+            const float fo = m == -INFINITY ? 0.0f : ex2_approx(m - mn);
+            const float fn = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mn);
+            l = __fmaf_rn(x.y, fn, l * fo);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = __fmaf_rn(a[i], fn, v[i] * fo);
+            m = mn;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            part[warp][lane * E + i] = v[i];
+        if (lane == 0)
+            part_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp == 0) {
+            float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                mm = fmaxf(mm, part_ml[i].x);
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float f = part_ml[k].x == -INFINITY ? 0.0f : ex2_approx(part_ml[k].x - mm);
+                ll = __fmaf_rn(part_ml[k].y, f, ll);
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    v[i] = __fmaf_rn(part[k][lane * E + i], f, v[i]);
+            }
+            const int32_t r = d.r0 + lr, tok = r / p.share;
+            paged_store_row<D>(p, v, ll, d.q0 + tok, d.head0 + r - tok * p.share, lane);
+        }
+        __syncthreads();
     }
 }
 

@@ -116,7 +116,44 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     return launch_status();
 }
 
-int64_t paged_workspace() { return 256; }
+// The workspace of one call: what the blocks of the two kernels say of their last segment, then
+// the pieces of both (two a block).
+constexpr int64_t kPagedDescBytes = (static_cast<int64_t>(kFewPerSm) * kPagedMaxSms * sizeof(FewDesc) + 255) / 256 * 256;
+
+template <int D>
+int64_t few_piece_bytes() { return 2ll * kFewPerSm * kPagedMaxSms * few_piece_floats<D>() * 4; }
+
+int64_t paged_workspace(int64_t D)
+{
+    return kPagedDescBytes + (D == 128 ? few_piece_bytes<128>() : few_piece_bytes<64>());
+}
+
+template <int D>
+sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, uint8_t *ws, cudaStream_t cs)
+{
+    const int sms = dev.sm_count < kPagedMaxSms ? dev.sm_count : kPagedMaxSms;
+    const uint32_t page = 1u << p.page_shift;
+    const uint64_t pool_rows = static_cast<uint64_t>(p.pages > 0 ? p.pages : 1) * p.Hkv * 2 * page;
+    const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap map_few;
+    if (!make_tmap_2d(&map_few, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D,
+                      page <= kFewTile ? 2 * page : kFewTile, swizzle))
+        return SDNQ_ERR_CUDA;
+    static PerDeviceCache<1> smem_few;
+    if (!smem_attr_once(smem_few, dev.index, attn_few_kernel<D>, FewConfig<D>::SMEM_BYTES)) {
+        cudaGetLastError();
+        return SDNQ_ERR_CUDA;
+    }
+    p.desc = ws;
+    p.partial = reinterpret_cast<float *>(ws + kPagedDescBytes);
+    p.rows_min = 0;
+    p.rows_max = INT32_MAX;
+    p.least_tiles = 4;
+    const unsigned blocks = static_cast<unsigned>(kFewPerSm * sms);
+    launch_programmatic(attn_few_kernel<D>, dim3(blocks), dim3(kFewThreads), FewConfig<D>::SMEM_BYTES, cs, map_few, p);
+    launch_programmatic(attn_join_kernel<D, kFewRows>, dim3(blocks, 2), dim3(kJoinThreads), 0, cs, p);
+    return launch_status();
+}
 
 // Largest context, window and sink count that the kernels' 32-bit positions hold.
 constexpr int64_t kPagedMaxKeys = 1ll << 30;
@@ -146,7 +183,7 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     if (ldq % 8 != 0 || ldo % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
         !aligned(lens, 4) || !aligned(table, 4) || !aligned(ws, 256))
         return SDNQ_ERR_ALIGN;
-    if (work && ws_bytes < paged_workspace())
+    if (work && ws_bytes < paged_workspace(D))
         return SDNQ_ERR_SHAPE;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != SDNQ_OK)
@@ -179,10 +216,10 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     p.scale = scale;
     p.c_g = rotation_factor(g);
     cudaGetLastError();
-    const unsigned blocks = static_cast<unsigned>((T * H + 3) / 4);
-    launch_programmatic(D == 128 ? attn_paged_kernel<128> : attn_paged_kernel<64>, dim3(blocks),
-                        dim3(128), 0, static_cast<cudaStream_t>(stream), p);
-    return launch_status();
+    p.timeout_ns = kDefaultTimeoutNs;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return D == 128 ? launch_paged<128>(p, dev, static_cast<uint8_t *>(ws), cs)
+                    : launch_paged<64>(p, dev, static_cast<uint8_t *>(ws), cs);
 }
 
 } // namespace
@@ -212,7 +249,7 @@ SDNQ_API int64_t sdnq_attention_paged_workspace(int64_t H, int64_t Hkv, int64_t 
 {
     if (H < 1 || Hkv < 1 || H % Hkv != 0 || (D != 64 && D != 128))
         return -1;
-    return sdnq::paged_workspace();
+    return sdnq::paged_workspace(D);
 }
 
 SDNQ_API sdnq_status sdnq_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,
