@@ -314,12 +314,12 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
 // Decoding: up to 16 query rows share a kv head, every key and value byte is used once, and
 // the kernel is bound by reading them. Per key and kv head 2 (D + 4) bytes arrive; at the
 // copy rate of the chip an SM gets about 24 bytes a cycle, so a key of D = 128 may take about
-// 11 cycles. The small matrix instructions (mma.sync) keep up with that easily at 16 rows,
-// and their register operands allow each warp to work alone:
-// - a producer warp streams tiles of 64 keys through a ring of 4 stages (one box of the page
-//   holds keys and values; 64-key pages make one copy of 16 KB), across segment borders, so the
-//   ring stays full while a segment is being finished;
-// - 4 warps take 16 keys of each tile each, with their own running maximum, sum and output
+// 11 cycles. The small matrix instructions (mma.sync) keep up with that at 16 rows, and their
+// register operands allow each warp to work alone:
+// - a producer warp streams tiles of 128 keys through a ring of 3 stages (one box holds the
+//   keys and the values of a page, or of 64 keys of a larger one), across segment borders, so
+//   the ring stays full while a segment is being finished;
+// - 4 warps take 32 keys of each tile each, with their own running maximum, sum and output
 //   (16 x D fp32 in registers): S = q k^T in int8 (m16n8k32), the exponentials, and
 //   O += (p s_v) v with v's codes turned into bf16 in registers (m16n8k16). They meet only at
 //   the end of a segment.
@@ -331,9 +331,10 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
 // swizzle. A lane's value column n of block j is dim (D / 8) n + j, its key bytes are 16-byte
 // chunks: any order of the contracted index serves as long as both operands follow it.
 
-constexpr int kFewTile = 64;      // keys per stage
+constexpr int kFewTile = 128;     // keys per stage
+constexpr int kFewBox = 64;       // keys of a box
 constexpr int kFewRows = 16;      // query rows of a tile
-constexpr int kFewStages = 4;
+constexpr int kFewStages = 3;
 constexpr int kFewThreads = 160;  // 4 warps and the producer
 constexpr int kPagedMaxSms = 160; // the workspace's size assumes no more
 constexpr int kFewPerSm = 2;
@@ -341,17 +342,18 @@ constexpr int kFewPerSm = 2;
 template <int D>
 struct FewConfig {
     static constexpr int STAGE = 2 * kFewTile * D;              // codes of a stage
-    static constexpr int SC_OFF = kFewStages * STAGE;           // scales: 2 * 64 fp32 a stage
+    static constexpr int SC_OFF = kFewStages * STAGE;           // scales: 2 * 128 fp32 a stage
     static constexpr int O_OFF = SC_OFF + kFewStages * 2 * kFewTile * 4;
     static constexpr int O_LD = D + 4;                          // floats
-    static constexpr int Q_OFF = O_OFF + 4 * kFewRows * O_LD * 4;
+    static constexpr int Q_OFF = O_OFF + kFewRows * O_LD * 4;
     static constexpr int QS_OFF = Q_OFF + kFewRows * D;
     static constexpr int ML_OFF = QS_OFF + kFewRows * 4;        // [4 warps][16 rows] (m, l)
     static constexpr int BAR_OFF = ML_OFF + 4 * kFewRows * 8;
-    static constexpr int META_OFF = BAR_OFF + 2 * kFewStages * 8;   // valid pages of each stage
-    static constexpr int SCAN_OFF = META_OFF + kFewStages * 4;
-    static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 64;
-    static_assert(BAR_OFF % 8 == 0 && kFewPerSm * (SMEM_BYTES + 1024) <= 228 * 1024,
+    static constexpr int META_OFF = BAR_OFF + 2 * kFewStages * 8;   // valid boxes of each stage
+    static constexpr int SCAN_OFF = META_OFF + 16;
+    static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 16;
+    static_assert(BAR_OFF % 8 == 0 && META_OFF % 4 == 0 && kFewStages * 4 <= 16 &&
+                      kFewPerSm * (SMEM_BYTES + 1024 + 128) <= 228 * 1024,
                   "shared memory per SM");
 };
 
@@ -385,17 +387,18 @@ __device__ __forceinline__ void mma_m16n8k16_bf16(float (&d)[4], uint32_t a0, ui
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Byte `j` of a and of b, two int8 codes, as a bf16 pair (a low), exactly. With m the low 7
-// bits and s the sign bit of a code, its value is (128 + m) - (128 or 256 by s); 0x4300 | m and
-// 0x4300 | (s << 7) are the bf16 patterns of the two.
+// Byte `j` of a and of b, two int8 codes, as a bf16 pair (a low), exactly, times 2^-6. With
+// u = code + 128, the bf16 pattern 0x00uu is u 2^-133 (subnormal numbers and the first binade
+// have one spacing), so one fused multiply-add gives u 2^-6 - 2.
+constexpr float kCodeUnit = 64.0f;
 __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t a, uint32_t b, int j)
 {
     const uint32_t pick = static_cast<uint32_t>(j) * 0x1111u + 0x4400u;
-    const uint32_t t = __byte_perm(a, b, pick);   // bytes a_j, a_j, b_j, b_j; 0 and 2 are used
-    uint32_t hi = (t & 0x007f007fu) | 0x43004300u, lo = (t & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&hi),
-                                     *reinterpret_cast<__nv_bfloat162 *>(&lo));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    // bytes a_j, a_j, b_j, b_j
+    const uint32_t t = (__byte_perm(a, b, pick) & 0x00ff00ffu) ^ 0x00800080u;
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(t), "r"(0x7f007f00u), "r"(0xc000c000u));
+    return r;
 }
 
 __device__ __forceinline__ uint4 lds_u4(uint32_t addr)
@@ -414,6 +417,11 @@ __device__ __forceinline__ float lds_f(uint32_t addr)
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+
+template <bool V>
+struct PagedFlag {
+    static constexpr bool value = V;
+};
 
 // Barrier of the four warps that compute.
 __device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -453,8 +461,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     __shared__ int abort_flag;
     volatile int *abort = &abort_flag;
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-    auto full = [&](int s) { return base + C::BAR_OFF + 8u * s; };
-    auto empty = [&](int s) { return base + C::BAR_OFF + 8u * (NST + s); };
+    auto full = [&](uint32_t s) { return base + C::BAR_OFF + 8u * s; };
+    auto empty = [&](uint32_t s) { return base + C::BAR_OFF + 8u * (NST + s); };
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
 
     if (threadIdx.x == 0) {
@@ -471,41 +479,39 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 
     int64_t first, per, total;
     PagedWalk w;
-    find_share<kFewTile, kFewRows, kFewThreads>(p, gridDim.x, p.least_tiles, reinterpret_cast<int32_t *>(smem + C::SCAN_OFF),
-                                                first, per, total, w);   // also: barriers initialised
+    find_share<kFewTile, kFewRows, kFewThreads>(p, gridDim.x, p.least_tiles,
+                                                reinterpret_cast<int32_t *>(smem + C::SCAN_OFF), first, per,
+                                                total, w);   // also: barriers initialised
     FewDesc *desc = reinterpret_cast<FewDesc *>(p.desc) + blockIdx.x;
     if (first >= total) {
         if (threadIdx.x == 0)
             desc->pieces = 0;
         return;
     }
-    const int64_t last = min(first + per, total);
-    const int64_t count = last - first;
-    const int32_t pp = min(1 << p.page_shift, kFewTile);        // keys of a page in a tile
+    const int64_t count = min(first + per, total) - first;
+    const int32_t pp = min(1 << p.page_shift, kFewBox);         // keys of a box
     const int32_t pp_shift = min(p.page_shift, 6);
-    const int32_t nchunk = kFewTile >> pp_shift;
+    const int32_t nbox = kFewTile >> pp_shift;
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
-        const int32_t tile_shift = 6 - p.page_shift;            // < 0: several tiles a page
         int64_t n = 0;
+        uint32_t st = 0, phase = 1;
         bool ok = true;
         while (ok && n < count) {
-            const int32_t kvh = w.kvh;
             const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
             const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
-            // Page ids are read 32 at a time, a batch ahead of their use; entry e is chunk
-            // e % nchunk of the piece's tile e / nchunk.
+            // Page ids are read 32 at a time, a batch ahead of their use; entry e is box
+            // e % nbox of the piece's tile e / nbox.
             auto fetch = [&](int32_t e0) {
                 const int32_t e = e0 + static_cast<int32_t>(lane);
-                const int32_t i = w.i + e / nchunk;
+                const int32_t i = w.i + e / nbox;
                 if (i >= w.i + tiles)
                     return -1;
-                const int32_t tile = i < w.t.ns ? i : w.t.w0 + i - w.t.ns;
-                const int32_t j = tile * kFewTile + (e % nchunk) * pp;
+                const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kFewTile + (e % nbox) * pp;
                 if (j >= w.s.len)
                     return -1;
-                const int32_t id = row[tile_shift >= 0 ? j >> p.page_shift : tile >> -tile_shift];
+                const int32_t id = row[j >> p.page_shift];
                 if (id < 0 || id >= p.pages) {
                     atomicOr(&g_device_error, kDevIndex);
                     return -1;
@@ -514,20 +520,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             };
             int32_t ids = fetch(0), ids_next = fetch(32), e0 = 0;
             for (int32_t k = 0; k < tiles; ++k, ++n) {
-                const int st = static_cast<int>(n % NST);
-                if (k * nchunk >= e0 + 32) {
+                if (k * nbox >= e0 + 32) {
                     ids = ids_next;
                     e0 += 32;
                     ids_next = fetch(e0 + 32);
                 }
-                // lane c < nchunk has page chunk c of this tile
-                const int32_t id = __shfl_sync(0xffffffffu, ids, (k * nchunk - e0 + static_cast<int32_t>(lane)) & 31);
-                const bool mine = static_cast<int32_t>(lane) < nchunk && id >= 0;
+                // lane c < nbox has box c of this tile
+                const int32_t id = __shfl_sync(0xffffffffu, ids, (k * nbox - e0 + static_cast<int32_t>(lane)) & 31);
+                const bool mine = static_cast<int32_t>(lane) < nbox && id >= 0;
                 const uint32_t valid = __ballot_sync(0xffffffffu, mine);
                 bool got = true;
                 if (lane == 0)
-                    got = mbar_wait_bounded(empty(st), (static_cast<uint32_t>(n / NST) & 1u) ^ 1u, abort,
-                                            p.timeout_ns);
+                    got = mbar_wait_bounded(empty(st), phase, abort, p.timeout_ns);
                 if (!__shfl_sync(0xffffffffu, static_cast<int>(got), 0)) {
                     ok = false;
                     break;
@@ -538,23 +542,24 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                 }
                 __syncwarp();
                 if (mine) {
-                    const int32_t i = w.i + k;
-                    const int32_t tile = i < w.t.ns ? i : w.t.w0 + i - w.t.ns;
-                    const int32_t prow = static_cast<int32_t>(((static_cast<int64_t>(id) * p.Hkv + kvh) * 2) << p.page_shift);
+                    const int32_t prow = static_cast<int32_t>(((static_cast<int64_t>(id) * p.Hkv + w.kvh) * 2) << p.page_shift);
                     const uint32_t dst = base + st * C::STAGE + lane * 2u * pp * D;
                     const uint32_t sdst = base + C::SC_OFF + (st * 2 * kFewTile + lane * 2 * pp) * 4;
-                    if (tile_shift >= 0) {     // the chunk is the page: its keys, then its values
+                    if (p.page_shift <= 6) {     // the box is the page: its keys, then its values
                         tma_load_2d(dst, &tmPool, full(st), 0, prow);
                         bulk_load_1d(sdst, p.scales + prow, 8u * pp, full(st));
                     } else {
-                        const int32_t off = (tile * kFewTile) & ((1 << p.page_shift) - 1);
-                        const int32_t vrow = prow + (1 << p.page_shift);
-                        tma_load_2d(dst, &tmPool, full(st), 0, prow + off);
-                        tma_load_2d(dst + kFewTile * D, &tmPool, full(st), 0, vrow + off);
-                        bulk_load_1d(sdst, p.scales + prow + off, 4u * pp, full(st));
-                        bulk_load_1d(sdst + 4 * pp, p.scales + vrow + off, 4u * pp, full(st));
+                        const int32_t i = w.i + k;
+                        const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kFewTile + static_cast<int32_t>(lane) * pp;
+                        const int32_t krow = prow + (j & ((1 << p.page_shift) - 1)), vrow = krow + (1 << p.page_shift);
+                        tma_load_2d(dst, &tmPool, full(st), 0, krow);
+                        tma_load_2d(dst + kFewBox * D, &tmPool, full(st), 0, vrow);
+                        bulk_load_1d(sdst, p.scales + krow, 4u * pp, full(st));
+                        bulk_load_1d(sdst + 4 * pp, p.scales + vrow, 4u * pp, full(st));
                     }
                 }
+                if (++st == NST)
+                    st = 0, phase ^= 1u;
             }
             walk_next_segment<kFewTile, kFewRows>(p, w);
         }
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         if (lane == 0) {
             volatile int no_abort = 0;
             for (int64_t j = n - NST < 0 ? 0 : n - NST; j < n; ++j)
-                mbar_wait_bounded(full(static_cast<int>(j % NST)), static_cast<uint32_t>(j / NST) & 1u, &no_abort,
+                mbar_wait_bounded(full(static_cast<uint32_t>(j % NST)), static_cast<uint32_t>(j / NST) & 1u, &no_abort,
                                   p.timeout_ns);
         }
         return;
@@ -572,52 +577,66 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     const uint32_t g = lane >> 2, t = lane & 3u;
     const uint32_t e = 2u * t + (t >> 1);                         // PI(2t)
     const uint32_t krow_n = (2u * (g >> 1) + (g >> 2)) ^ ((g & 1u) << 2);   // PI(g)
-    const int32_t my_key = static_cast<int32_t>(warp) * 16;
-    const uint32_t my_chunk = static_cast<uint32_t>(my_key >> pp_shift);
-    const uint32_t my_krow = my_chunk * 2u * pp + (my_key & (pp - 1));
+    const int32_t my_key = static_cast<int32_t>(warp) * 32;
+    // boxes and box rows of this warp's two runs of 16 keys
+    const uint32_t my_box[2] = {static_cast<uint32_t>(my_key >> pp_shift), static_cast<uint32_t>((my_key + 16) >> pp_shift)};
+    const uint32_t my_row[2] = {my_box[0] * 2u * pp + (my_key & (pp - 1)),
+                                my_box[1] * 2u * pp + ((my_key + 16) & (pp - 1))};
+    const uint32_t my_boxes = (1u << my_box[0]) | (1u << my_box[1]);
     float *obuf = reinterpret_cast<float *>(smem + C::O_OFF);
     float2 *ml = reinterpret_cast<float2 *>(smem + C::ML_OFF);
     float *qs = reinterpret_cast<float *>(smem + C::QS_OFF);
     bool ok = true;
     int64_t n = 0;
+    uint32_t st = 0, phase = 0;
     int piece_no = 0;
     while (n < count) {
         const int32_t r0 = w.q * kFewRows, head0 = w.kvh * p.share;
         const int32_t rows = min(kFewRows, w.s.n * p.share - r0);
         const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
-        // this warp's four query rows: codes and scales
-#pragma unroll 1
-        for (int rr = 0; rr < 4; ++rr) {
-            const int32_t lr = static_cast<int32_t>(warp) * 4 + rr, r = r0 + lr;
-            float v[E];
+        const bool two = rows > 8;       // rows 8..15 are in use
+        // query rows warp, warp + 4, ...: codes and scales (rows past the last: zeros)
+        {
+            uint32_t x[4][E / 2];
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                v[i] = 0.0f;
-            if (lr < rows) {
-                const int32_t ti = r / p.share;
-                const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + ti) * p.ldq +
-                                    static_cast<int64_t>(head0 + r - ti * p.share) * D + lane * E;
-                uint32_t x[E / 2];
-                if (E == 4) {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(q);
-                    x[0] = a.x, x[E / 2 - 1] = a.y;
-                } else {
-                    x[0] = *reinterpret_cast<const uint32_t *>(q);
-                }
+            for (int rr = 0; rr < 4; ++rr) {
+                const int32_t lr = rr * 4 + static_cast<int32_t>(warp), r = r0 + lr;
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    v[2 * i] = __uint_as_float(x[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+                for (int i = 0; i < E / 2; ++i)
+                    x[rr][i] = 0u;
+                if (lr < rows) {
+                    const int32_t ti = r / p.share;
+                    const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + ti) * p.ldq +
+                                        static_cast<int64_t>(head0 + r - ti * p.share) * D + lane * E;
+                    if (E == 4) {
+                        const uint2 a = *reinterpret_cast<const uint2 *>(q);
+                        x[rr][0] = a.x, x[rr][E / 2 - 1] = a.y;
+                    } else {
+                        x[rr][0] = *reinterpret_cast<const uint32_t *>(q);
+                    }
                 }
             }
-            float sq;
-            const uint32_t c = warp_quant_row<E>(v, p.group, p.c_g, lane, sq);
-            if (E == 4)
-                *reinterpret_cast<uint32_t *>(smem + C::Q_OFF + lr * D + lane * E) = c;
-            else
-                *reinterpret_cast<uint16_t *>(smem + C::Q_OFF + lr * D + lane * E) = static_cast<uint16_t>(c);
-            if (lane == 0)
-                qs[lr] = sq;
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) {
+                const int32_t lr = rr * 4 + static_cast<int32_t>(warp);
+                uint32_t c = 0u;
+                float sq = 0.0f;
+                if (lr < rows) {
+                    float v[E];
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) {
+                        v[2 * i] = __uint_as_float(x[rr][i] << 16);
+                        v[2 * i + 1] = __uint_as_float(x[rr][i] & 0xffff0000u);
+                    }
+                    c = warp_quant_row<E>(v, p.group, p.c_g, lane, sq);
+                }
+                if (E == 4)
+                    *reinterpret_cast<uint32_t *>(smem + C::Q_OFF + lr * D + lane * E) = c;
+                else
+                    *reinterpret_cast<uint16_t *>(smem + C::Q_OFF + lr * D + lane * E) = static_cast<uint16_t>(c);
+                if (lane == 0)
+                    qs[lr] = sq;
+            }
         }
         few_sync();
         uint4 qa[2][H2];     // rows g and g + 8, 16-byte chunk t of each 64-element half
@@ -636,6 +655,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         }
         const int32_t pos_first = w.s.len - w.s.n + r0 / p.share;
         const int32_t pos_last = w.s.len - w.s.n + (r0 + rows - 1) / p.share;
+        const int32_t low_first = p.window > 0 ? pos_first - p.window + 1 : INT32_MIN;
         const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : INT32_MIN;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
         float o[DB][4];
@@ -646,121 +666,111 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                 o[j][i] = 0.0f;
 
 #pragma unroll 1
-        for (int32_t k = 0; k < tiles; ++k, ++n) {
-            const int st = static_cast<int>(n % NST);
+        for (int32_t k = 0; k < tiles; ++k) {
             const int32_t ti = w.i + k;
             const int32_t j0 = (ti < w.t.ns ? ti : w.t.w0 + ti - w.t.ns) * kFewTile + my_key;
-            const bool got = ok && mbar_wait_bounded(full(st), static_cast<uint32_t>(n / NST) & 1u, abort,
-                                                     p.timeout_ns);
+            const bool got = ok && mbar_wait_bounded(full(st), phase, abort, p.timeout_ns);
             ok = __all_sync(0xffffffffu, got);
-            if (ok) {
-                const bool there = ((meta[st] >> my_chunk) & 1u) != 0u;
-                // nothing of these 16 keys is visible to any row: leave them
-                const bool some = there && j0 <= pos_last &&
-                                  (j0 + 15 >= (p.window > 0 ? pos_first - p.window + 1 : INT32_MIN) ||
-                                   j0 < p.sinks);
-                if (some) {
-                    const uint32_t codes = base + st * C::STAGE + my_krow * D;
-                    const uint32_t sc = base + C::SC_OFF + (st * 2 * kFewTile + my_krow) * 4;
-                    int32_t acc[2][4];
-                    uint4 kb[2][H2];
+            // nothing of these 32 keys is visible to any row: leave them
+            if (ok && j0 <= pos_last && (j0 + 31 >= low_first || j0 < p.sinks)) {
+                const uint32_t there = meta[st];
+                const bool whole = j0 + 31 <= pos_first && (j0 >= low_last || j0 + 32 <= p.sinks) &&
+                                   (there & my_boxes) == my_boxes;
+                const uint32_t codes[2] = {base + st * C::STAGE + my_row[0] * D, base + st * C::STAGE + my_row[1] * D};
+                const uint32_t sc = base + C::SC_OFF + st * 2 * kFewTile * 4;
+                float y[4][4];
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
+                for (int nb = 0; nb < 4; ++nb) {
+                    int32_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-                        for (int h = 0; h < H2; ++h) {
-                            const uint32_t sw = D == 128 ? (t + 4u * h) ^ krow_n : t ^ (krow_n >> 1);
-                            kb[nb][h] = lds_u4(codes + (8u * nb + krow_n) * D + sw * 16u);
-                        }
-#pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            acc[nb][i] = 0;
-#pragma unroll
-                        for (int h = 0; h < H2; ++h) {
-                            mma_m16n8k32_s8(acc[nb], qa[0][h].x, qa[1][h].x, qa[0][h].y, qa[1][h].y,
-                                            kb[nb][h].x, kb[nb][h].y);
-                            mma_m16n8k32_s8(acc[nb], qa[0][h].z, qa[1][h].z, qa[0][h].w, qa[1][h].w,
-                                            kb[nb][h].z, kb[nb][h].w);
-                        }
+                    for (int h = 0; h < H2; ++h) {
+                        const uint32_t sw = D == 128 ? (t + 4u * h) ^ krow_n : t ^ (krow_n >> 1);
+                        const uint4 kb = lds_u4(codes[nb >> 1] + (8u * (nb & 1) + krow_n) * D + sw * 16u);
+                        mma_m16n8k32_s8(acc, qa[0][h].x, qa[1][h].x, qa[0][h].y, qa[1][h].y, kb.x, kb.y);
+                        mma_m16n8k32_s8(acc, qa[0][h].z, qa[1][h].z, qa[0][h].w, qa[1][h].w, kb.z, kb.w);
                     }
-                    // acc[nb][2u + c]: row g + 8u, key 8 nb + PI(2t + c)
-                    float sk[2][2], sv[2][2], y[2][4];
+                    // acc[2u + c]: row g + 8u, key 8 nb + PI(2t + c)
+                    const uint32_t a = sc + (my_row[nb >> 1] + 8u * (nb & 1)) * 4u;
+                    const float sk0 = lds_f(a + e * 4u), sk1 = lds_f(a + (e ^ 4u) * 4u);
+                    y[nb][0] = static_cast<float>(acc[0]) * sk0, y[nb][1] = static_cast<float>(acc[1]) * sk1;
+                    y[nb][2] = static_cast<float>(acc[2]) * sk0, y[nb][3] = static_cast<float>(acc[3]) * sk1;
+                }
+                if (!whole) {
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
+                    for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t a = sc + (8u * nb + (c ? e ^ 4u : e)) * 4u;
-                            sk[nb][c] = lds_f(a);
-                            sv[nb][c] = lds_f(a + 4u * pp);
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t j = j0 + 8 * nb + static_cast<int32_t>((i & 1) ? e ^ 4u : e);
+                            const bool see = j <= pos[i >> 1] && (j >= low[i >> 1] || j < p.sinks) &&
+                                             ((there >> my_box[nb >> 1]) & 1u) != 0u;
+                            y[nb][i] = see ? y[nb][i] : -INFINITY;
                         }
+                }
+                float alpha[2] = {1.0f, 1.0f};
+                bool grew = false;
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
+                for (int u = 0; u < 2; ++u) {
+                    if (u == 1 && !two)
+                        break;
+                    float mx = fmaxf(max3f(y[0][2 * u], y[0][2 * u + 1], y[1][2 * u]),
+                                     max3f(y[1][2 * u + 1], y[2][2 * u], y[2][2 * u + 1]));
+                    mx = max3f(mx, y[3][2 * u], y[3][2 * u + 1]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mb = mx * row_f[u];
+                    // the sums are rescaled only when the maximum grows by more than 2^8
+                    const bool grow = mb > m[u] + 8.0f;
+                    alpha[u] = grow ? ex2_approx(m[u] - mb) : 1.0f;
+                    m[u] = grow ? mb : m[u];
+                    grew |= grow;
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+                    l[0] *= alpha[0];
+                    l[1] *= alpha[1];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            y[nb][i] = static_cast<float>(acc[nb][i]) * sk[nb][i & 1];
-                    const bool whole = j0 + 15 <= pos_first && (j0 >= low_last || j0 + 16 <= p.sinks);
-                    uint32_t hidden = 0u;
-                    if (!whole) {
-#pragma unroll
-                        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int32_t j = j0 + 8 * nb + static_cast<int32_t>((i & 1) ? e ^ 4u : e);
-                                const bool see = j <= pos[i >> 1] && (j >= low[i >> 1] || j < p.sinks);
-                                if (!see) {
-                                    y[nb][i] = -INFINITY;
-                                    hidden |= 1u << (nb * 4 + i);
-                                }
-                            }
+                    for (int j = 0; j < DB; ++j) {
+                        mul2(o[j][0], o[j][1], o[j][0], o[j][1], alpha[0], alpha[0]);
+                        mul2(o[j][2], o[j][3], o[j][2], o[j][3], alpha[1], alpha[1]);
                     }
-                    float alpha[2];
-                    bool grew = false;
+                }
+                uint32_t pa[4][2] = {};   // [nb][u]: probabilities times s_v, a bf16 pair
+                auto weigh = [&](auto masked) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float mx = fmaxf(fmaxf(y[0][2 * u], y[0][2 * u + 1]), fmaxf(y[1][2 * u], y[1][2 * u + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float mb = mx * row_f[u];
-                        // the sums are rescaled only when the maximum grows by more than 2^8
-                        const bool grow = mb > m[u] + 8.0f;
-                        alpha[u] = grow ? ex2_approx(m[u] - mb) : 1.0f;
-                        m[u] = grow ? mb : m[u];
-                        grew |= grow;
-                    }
-                    if (__any_sync(0xffffffffu, grew)) {
-                        l[0] *= alpha[0];
-                        l[1] *= alpha[1];
+                    for (int nb = 0; nb < 4; ++nb) {
+                        const uint32_t a = sc + (my_row[nb >> 1] + 8u * (nb & 1) + pp) * 4u;
+                        const float sv[2] = {lds_f(a + e * 4u), lds_f(a + (e ^ 4u) * 4u)};
 #pragma unroll
-                        for (int j = 0; j < DB; ++j) {
-                            mul2(o[j][0], o[j][1], o[j][0], o[j][1], alpha[0], alpha[0]);
-                            mul2(o[j][2], o[j][3], o[j][2], o[j][3], alpha[1], alpha[1]);
-                        }
-                    }
-                    uint32_t pa[2][2];   // [nb][u]: probabilities times s_v, a bf16 pair
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float neg_m = m[u] == -INFINITY ? 0.0f : -m[u];
-#pragma unroll
-                        for (int nb = 0; nb < 2; ++nb) {
+                        for (int u = 0; u < 2; ++u) {
+                            if (u == 1 && !two)
+                                break;
+                            const float neg_m = m[u] == -INFINITY ? 0.0f : -m[u];
                             float pr[2];
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const float x = ex2_approx(__fmaf_rn(y[nb][2 * u + c], row_f[u], neg_m));
                                 l[u] += x;
+                                pr[c] = x * sv[c];
                                 // a hidden key adds 0 whatever its scale holds
-                                pr[c] = (hidden >> (nb * 4 + 2 * u + c)) & 1u ? 0.0f : x * sv[nb][c];
+                                if (decltype(masked)::value)
+                                    pr[c] = x == 0.0f ? 0.0f : pr[c];
                             }
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
                             pa[nb][u] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
                     }
-                    // values of keys PI(2t), PI(2t+1) of both 8-key blocks, this lane's DB dims
+                };
+                if (whole)
+                    weigh(PagedFlag<false>());
+                else
+                    weigh(PagedFlag<true>());
+                // values of keys PI(2t), PI(2t+1) of two 8-key blocks, this lane's DB dims
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb) {
                     uint32_t vb[4][DB / 4];
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t kr = (kk & 1) ? e ^ 4u : e;
-                        const uint32_t row = codes + (pp + 8u * (kk >> 1) + kr) * D;
+                        const uint32_t row = codes[hb] + (pp + 8u * (kk >> 1) + kr) * D;
                         if (D == 128) {
                             const uint4 a = lds_u4(row + ((g ^ kr) << 4));
                             vb[kk][0] = a.x, vb[kk][1] = a.y, vb[kk][DB / 4 - 2] = a.z, vb[kk][DB / 4 - 1] = a.w;
@@ -774,16 +784,20 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                     for (int j = 0; j < DB; ++j) {
                         const uint32_t b0 = codes_to_bf16x2(vb[0][j >> 2], vb[1][j >> 2], j & 3);
                         const uint32_t b1 = codes_to_bf16x2(vb[2][j >> 2], vb[3][j >> 2], j & 3);
-                        mma_m16n8k16_bf16(o[j], pa[0][0], pa[0][1], pa[1][0], pa[1][1], b0, b1);
+                        mma_m16n8k16_bf16(o[j], pa[2 * hb][0], pa[2 * hb][1], pa[2 * hb + 1][0], pa[2 * hb + 1][1], b0, b1);
                     }
                 }
             }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty(st));
+            if (++st == NST)
+                st = 0, phase ^= 1u;
         }
+        n += tiles;
 
         // ------------------------------------------------ join the four warps' sums
+        // the maximum over the warps first; then one warp after the other adds its sums
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
@@ -791,47 +805,56 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             if (t == 0)
                 ml[warp * kFewRows + g + 8 * u] = make_float2(m[u], l[u]);
         }
+        few_sync();
+        float scale_o[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float mm = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mm = fmaxf(mm, ml[i * kFewRows + g + 8 * u].x);
+            scale_o[u] = m[u] == -INFINITY ? 0.0f : kCodeUnit * ex2_approx(m[u] - mm);
+        }
         // lane (g, t): dims [2 DB t, 2 DB (t + 1)) of rows g and g + 8: o[j][0] is dim 2 DB t + j,
         // o[j][1] dim 2 DB t + DB + j
+#pragma unroll 1
+        for (uint32_t turn = 0; turn < 4; ++turn) {
+            if (turn == warp) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
+                    if (u == 1 && !two)
+                        break;
 #pragma unroll
-            for (int c = 0; c < 2 * DB / 4; ++c) {
-                float4 x;
-                const int hb = c / (DB / 4), jj = (c % (DB / 4)) * 4;
-                x.x = o[jj][2 * u + hb], x.y = o[jj + 1][2 * u + hb], x.z = o[jj + 2][2 * u + hb],
-                x.w = o[jj + 3][2 * u + hb];
-                *reinterpret_cast<float4 *>(obuf + (warp * kFewRows + g + 8 * u) * C::O_LD + 2 * DB * t +
-                                            4 * c) = x;
+                    for (int c = 0; c < 2 * DB / 4; ++c) {
+                        const int hb = c / (DB / 4), jj = (c % (DB / 4)) * 4;
+                        float4 *at = reinterpret_cast<float4 *>(obuf + (g + 8 * u) * C::O_LD + 2 * DB * t + 4 * c);
+                        float4 x = turn == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
+                        x.x = __fmaf_rn(o[jj][2 * u + hb], scale_o[u], x.x);
+                        x.y = __fmaf_rn(o[jj + 1][2 * u + hb], scale_o[u], x.y);
+                        x.z = __fmaf_rn(o[jj + 2][2 * u + hb], scale_o[u], x.z);
+                        x.w = __fmaf_rn(o[jj + 3][2 * u + hb], scale_o[u], x.w);
+                        *at = x;
+                    }
+                }
             }
-        few_sync();
+            few_sync();
+        }
         const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
         float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * few_piece_floats<D>();
 #pragma unroll 1
-        for (int rr = 0; rr < 4; ++rr) {
-            const int32_t lr = static_cast<int32_t>(warp) * 4 + rr;
-            if (lr >= rows)
-                break;
-            float2 x[4];
-            float mm = -INFINITY;
+        for (int32_t lr = static_cast<int32_t>(warp); lr < rows; lr += 4) {
+            float mm = -INFINITY, ll = 0.0f, v[E];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mm = fmaxf(mm, ml[i * kFewRows + lr].x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = ml[i * kFewRows + lr];
-                mm = fmaxf(mm, x[i].x);
+                const float2 x = ml[i * kFewRows + lr];
+                ll = __fmaf_rn(x.y, x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mm), ll);
             }
-            float ll = 0.0f, v[E];
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                v[i] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float f = x[i].x == -INFINITY ? 0.0f : ex2_approx(x[i].x - mm);
-                ll = __fmaf_rn(x[i].y, f, ll);
-                const float *src = obuf + (i * kFewRows + lr) * C::O_LD + lane * E;
-#pragma unroll
-                for (int d = 0; d < E; ++d)
-                    v[d] = __fmaf_rn(src[d], f, v[d]);
-            }
+                v[i] = obuf[lr * C::O_LD + lane * E + i];
             const int32_t r = r0 + lr, tok = r / p.share;
             if (begins && ends) {
                 if (ok)

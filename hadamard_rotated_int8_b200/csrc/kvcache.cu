@@ -137,7 +137,7 @@ sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, uint8_t *ws, cuda
     const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap map_few;
     if (!make_tmap_2d(&map_few, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D,
-                      page <= kFewTile ? 2 * page : kFewTile, swizzle))
+                      page <= kFewBox ? 2 * page : kFewBox, swizzle))
         return SDNQ_ERR_CUDA;
     static PerDeviceCache<1> smem_few;
     if (!smem_attr_once(smem_few, dev.index, attn_few_kernel<D>, FewConfig<D>::SMEM_BYTES)) {
@@ -148,7 +148,7 @@ sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, uint8_t *ws, cuda
     p.partial = reinterpret_cast<float *>(ws + kPagedDescBytes);
     p.rows_min = 0;
     p.rows_max = INT32_MAX;
-    p.least_tiles = 4;
+    p.least_tiles = 2;
     const unsigned blocks = static_cast<unsigned>(kFewPerSm * sms);
     launch_programmatic(attn_few_kernel<D>, dim3(blocks), dim3(kFewThreads), FewConfig<D>::SMEM_BYTES, cs, map_few, p);
     launch_programmatic(attn_join_kernel<D, kFewRows>, dim3(blocks, 2), dim3(kJoinThreads), 0, cs, p);
