@@ -311,56 +311,56 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
 
 // ---------------------------------------------------------------- few query rows
 //
-// Decoding: up to 16 query rows share a kv head, every key and value byte is used once, and
-// the kernel is bound by reading them. Per key and kv head 2 (D + 4) bytes arrive; at the
-// copy rate of the chip an SM gets about 24 bytes a cycle, so a key of D = 128 may take about
-// 11 cycles. The small matrix instructions (mma.sync) keep up with that at 16 rows, and their
-// register operands allow each warp to work alone:
-// - a producer warp streams tiles of 128 keys through a ring of 3 stages (one box holds the
-//   keys and the values of a page, or of 64 keys of a larger one), across segment borders, so
-//   the ring stays full while a segment is being finished;
-// - 4 warps take 32 keys of each tile each, with their own running maximum, sum and output
-//   (16 x D fp32 in registers): S = q k^T in int8 (m16n8k32), the exponentials, and
-//   O += (p s_v) v with v's codes turned into bf16 in registers (m16n8k16). They meet only at
-//   the end of a segment.
-// Two blocks per SM keep up to 132 KB in flight.
+// Decoding: up to 8 NB query rows (NB = 1, 2) share a kv head, every key and value byte is
+// used once, and the kernel is bound by reading them. Per key and kv head 2 (D + 4) bytes
+// arrive; at the copy rate of the chip an SM gets about 24 bytes a cycle, so a key of D = 128
+// may take about 11 cycles. The small matrix instructions (mma.sync) keep up with that, and
+// their register operands allow each warp to work alone:
+// - a producer warp streams tiles of 128 keys through a ring of stages (one box holds the keys
+//   and the values of a page, or of 64 keys of a larger one), across segment borders, so the
+//   ring stays full while a segment is being finished;
+// - 4 warps take 32 keys of each tile each, with their own running maximum, sum and output:
+//   S^T = k q^T in int8 (m16n8k32), the exponentials, P^T moved into operand form
+//   (movmatrix), and O^T += v^T (p s_v) with v's codes turned into bf16 in registers
+//   (m16n8k16). They meet only at the end of a segment.
+// Keys and dims, not query rows, fill the 16 rows of each instruction: with 8 query rows half
+// the instructions and accumulators of the other way round.
 //
-// Fragments. The key of column n of an 8-key block is PI(n), PI(2t) = 2t + (t >> 1) and
-// PI(2t + 1) = PI(2t) ^ 4, which makes both the keys' 16-byte loads (two keys' rows per
-// quarter warp) and the values' (four keys' rows) free of bank conflicts in the 128-byte
-// swizzle. A lane's value column n of block j is dim (D / 8) n + j, its key bytes are 16-byte
-// chunks: any order of the contracted index serves as long as both operands follow it.
+// Fragments. Row i of an 8-key block is key PI(i), PI(2t) = 2t + (t >> 1) and PI(2t + 1) =
+// PI(2t) ^ 4, which makes both the keys' 16-byte loads (two keys' rows per quarter warp) and
+// the values' (four keys' rows) free of bank conflicts in the 128-byte swizzle. Lane (g, t)
+// holds dims [(D / 8) g, (D / 8) (g + 1)) of the output: rows g and g + 8 of block j are its
+// dims 2j and 2j + 1; its key bytes are 16-byte chunks: any order of the contracted index
+// serves as long as both operands follow it.
 
 constexpr int kFewTile = 128;     // keys per stage
 constexpr int kFewBox = 64;       // keys of a box
-constexpr int kFewRows = 16;      // query rows of a tile
-constexpr int kFewStages = 3;
 constexpr int kFewThreads = 160;  // 4 warps and the producer
 constexpr int kPagedMaxSms = 160; // the workspace's size assumes no more
-constexpr int kFewPerSm = 2;
 
-template <int D>
+template <int D, int NB>
 struct FewConfig {
+    static constexpr int ROWS = 8 * NB;                         // query rows of a tile
+    static constexpr int PER_SM = NB == 1 ? 3 : 2;              // blocks, by registers
+    static constexpr int NST = NB == 1 ? 2 : 3;                 // stages
     static constexpr int STAGE = 2 * kFewTile * D;              // codes of a stage
-    static constexpr int SC_OFF = kFewStages * STAGE;           // scales: 2 * 128 fp32 a stage
-    static constexpr int O_OFF = SC_OFF + kFewStages * 2 * kFewTile * 4;
+    static constexpr int SC_OFF = NST * STAGE;                  // scales: 2 * 128 fp32 a stage
+    static constexpr int O_OFF = SC_OFF + NST * 2 * kFewTile * 4;
     static constexpr int O_LD = D + 4;                          // floats
-    static constexpr int Q_OFF = O_OFF + kFewRows * O_LD * 4;
-    static constexpr int QS_OFF = Q_OFF + kFewRows * D;
-    static constexpr int ML_OFF = QS_OFF + kFewRows * 4;        // [4 warps][16 rows] (m, l)
-    static constexpr int BAR_OFF = ML_OFF + 4 * kFewRows * 8;
-    static constexpr int META_OFF = BAR_OFF + 2 * kFewStages * 8;   // valid boxes of each stage
+    static constexpr int Q_OFF = O_OFF + ROWS * O_LD * 4;
+    static constexpr int QS_OFF = Q_OFF + ROWS * D;
+    static constexpr int ML_OFF = QS_OFF + ROWS * 4;            // [4 warps][ROWS] (m, l)
+    static constexpr int BAR_OFF = ML_OFF + 4 * ROWS * 8;
+    static constexpr int META_OFF = BAR_OFF + 2 * NST * 8;      // valid boxes of each stage
     static constexpr int SCAN_OFF = META_OFF + 16;
     static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 16;
-    static_assert(BAR_OFF % 8 == 0 && META_OFF % 4 == 0 && kFewStages * 4 <= 16 &&
-                      kFewPerSm * (SMEM_BYTES + 1024 + 128) <= 228 * 1024,
+    static_assert(BAR_OFF % 8 == 0 && META_OFF % 4 == 0 && NST * 4 <= 16 &&
+                      PER_SM * (SMEM_BYTES + 1024 + 128) <= 228 * 1024,
                   "shared memory per SM");
+    // Workspace: a piece's sums [ROWS][D], then its (m, l) [ROWS][2]; two pieces a block (0: of
+    // the segment that began before the block, 1: of the one that goes on behind it).
+    static constexpr int64_t PIECE = ROWS * (D + 2);
 };
-
-// Workspace: a piece's sums [16][D], then its (m, l) [16][2]; two pieces a block (0: of the
-// segment that began before the block, 1: of the one that goes on behind it).
-template <int D>
-__host__ __device__ constexpr int64_t few_piece_floats() { return kFewRows * (D + 2); }
 
 struct FewDesc {       // the segment that begins in a block and goes on behind it
     int32_t pieces;    // 0: none
@@ -411,6 +411,14 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t addr)
     return v;
 }
 
+// The 8x8 matrix of 16-bit values held two a lane (row lane / 4), transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
 __device__ __forceinline__ float lds_f(uint32_t addr)
 {
     float v;
@@ -448,12 +456,12 @@ __device__ __forceinline__ void paged_store_row(const PagedParams &p, float (&v)
         *reinterpret_cast<uint32_t *>(o) = w[0];
 }
 
-template <int D>
-__global__ void __launch_bounds__(kFewThreads, kFewPerSm)
+template <int D, int NB>
+__global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmPool, const PagedParams p)
 {
-    using C = FewConfig<D>;
-    constexpr int NST = kFewStages, E = D / 32, H2 = D / 64, DB = D / 8;
+    using C = FewConfig<D, NB>;
+    constexpr int NST = C::NST, ROWS = C::ROWS, E = D / 32, H2 = D / 64, DB = D / 16;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
 
     int64_t first, per, total;
     PagedWalk w;
-    find_share<kFewTile, kFewRows, kFewThreads>(p, gridDim.x, p.least_tiles,
+    find_share<kFewTile, ROWS, kFewThreads>(p, gridDim.x, p.least_tiles,
                                                 reinterpret_cast<int32_t *>(smem + C::SCAN_OFF), first, per,
                                                 total, w);   // also: barriers initialised
     FewDesc *desc = reinterpret_cast<FewDesc *>(p.desc) + blockIdx.x;
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                 if (++st == NST)
                     st = 0, phase ^= 1u;
             }
-            walk_next_segment<kFewTile, kFewRows>(p, w);
+            walk_next_segment<kFewTile, ROWS>(p, w);
         }
         // every copy has landed before the block may end (its consumers may have given up)
         if (lane == 0) {
@@ -591,15 +599,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
     uint32_t st = 0, phase = 0;
     int piece_no = 0;
     while (n < count) {
-        const int32_t r0 = w.q * kFewRows, head0 = w.kvh * p.share;
-        const int32_t rows = min(kFewRows, w.s.n * p.share - r0);
+        const int32_t r0 = w.q * ROWS, head0 = w.kvh * p.share;
+        const int32_t rows = min(ROWS, w.s.n * p.share - r0);
         const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
-        const bool two = rows > 8;       // rows 8..15 are in use
         // query rows warp, warp + 4, ...: codes and scales (rows past the last: zeros)
         {
-            uint32_t x[4][E / 2];
+            constexpr int RQ = ROWS / 4;
+            uint32_t x[RQ][E / 2];
 #pragma unroll
-            for (int rr = 0; rr < 4; ++rr) {
+            for (int rr = 0; rr < RQ; ++rr) {
                 const int32_t lr = rr * 4 + static_cast<int32_t>(warp), r = r0 + lr;
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i)
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                 }
             }
 #pragma unroll
-            for (int rr = 0; rr < 4; ++rr) {
+            for (int rr = 0; rr < RQ; ++rr) {
                 const int32_t lr = rr * 4 + static_cast<int32_t>(warp);
                 uint32_t c = 0u;
                 float sq = 0.0f;
@@ -639,31 +647,39 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             }
         }
         few_sync();
-        uint4 qa[2][H2];     // rows g and g + 8, 16-byte chunk t of each 64-element half
-        float row_f[2];
-        int32_t pos[2], low[2];
+        uint4 qb[NB][H2];    // query row g + 8 nb, 16-byte chunk t of each 64-element half
+        float row_f[NB][2];  // of query rows 8 nb + 2t, 2t + 1
+        int32_t pos[NB][2], low[NB][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int32_t lr = static_cast<int32_t>(g) + 8 * u;
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int h = 0; h < H2; ++h)
-                qa[u][h] = lds_u4(base + C::Q_OFF + lr * D + h * 64 + t * 16);
-            // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out (attention.cuh)
-            row_f[u] = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
-            pos[u] = w.s.len - w.s.n + (r0 + min(lr, rows - 1)) / p.share;
-            low[u] = p.window > 0 ? pos[u] - p.window + 1 : INT32_MIN;
+                qb[nb][h] = lds_u4(base + C::Q_OFF + (static_cast<int32_t>(g) + 8 * nb) * D + h * 64 + t * 16);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int32_t lr = 8 * nb + 2 * static_cast<int32_t>(t) + c;
+                // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out (attention.cuh)
+                row_f[nb][c] = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
+                pos[nb][c] = w.s.len - w.s.n + (r0 + min(lr, rows - 1)) / p.share;
+                low[nb][c] = p.window > 0 ? pos[nb][c] - p.window + 1 : INT32_MIN;
+            }
         }
         const int32_t pos_first = w.s.len - w.s.n + r0 / p.share;
         const int32_t pos_last = w.s.len - w.s.n + (r0 + rows - 1) / p.share;
         const int32_t low_first = p.window > 0 ? pos_first - p.window + 1 : INT32_MIN;
         const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : INT32_MIN;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-        float o[DB][4];
+        float m[NB][2], l[NB][2];
+        float o[NB][DB][4];
 #pragma unroll
-        for (int j = 0; j < DB; ++j)
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[j][i] = 0.0f;
+            for (int j = 0; j < DB; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[nb][j][i] = 0.0f;
+        }
 
 #pragma unroll 1
         for (int32_t k = 0; k < tiles; ++k) {
@@ -678,84 +694,97 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                                    (there & my_boxes) == my_boxes;
                 const uint32_t codes[2] = {base + st * C::STAGE + my_row[0] * D, base + st * C::STAGE + my_row[1] * D};
                 const uint32_t sc = base + C::SC_OFF + st * 2 * kFewTile * 4;
-                float y[4][4];
+                // y[nb][kb][c]: key 8 kb + PI(g), query row 8 nb + 2t + c
+                float y[NB][4][2];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    int32_t acc[4] = {0, 0, 0, 0};
+                for (int kk = 0; kk < 2; ++kk) {
+                    int32_t acc[NB][4] = {};
 #pragma unroll
                     for (int h = 0; h < H2; ++h) {
                         const uint32_t sw = D == 128 ? (t + 4u * h) ^ krow_n : t ^ (krow_n >> 1);
-                        const uint4 kb = lds_u4(codes[nb >> 1] + (8u * (nb & 1) + krow_n) * D + sw * 16u);
-                        mma_m16n8k32_s8(acc, qa[0][h].x, qa[1][h].x, qa[0][h].y, qa[1][h].y, kb.x, kb.y);
-                        mma_m16n8k32_s8(acc, qa[0][h].z, qa[1][h].z, qa[0][h].w, qa[1][h].w, kb.z, kb.w);
+                        const uint4 a = lds_u4(codes[kk] + krow_n * D + sw * 16u);
+                        const uint4 b = lds_u4(codes[kk] + (8u + krow_n) * D + sw * 16u);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma_m16n8k32_s8(acc[nb], a.x, b.x, a.y, b.y, qb[nb][h].x, qb[nb][h].y);
+                            mma_m16n8k32_s8(acc[nb], a.z, b.z, a.w, b.w, qb[nb][h].z, qb[nb][h].w);
+                        }
                     }
-                    // acc[2u + c]: row g + 8u, key 8 nb + PI(2t + c)
-                    const uint32_t a = sc + (my_row[nb >> 1] + 8u * (nb & 1)) * 4u;
-                    const float sk0 = lds_f(a + e * 4u), sk1 = lds_f(a + (e ^ 4u) * 4u);
-                    y[nb][0] = static_cast<float>(acc[0]) * sk0, y[nb][1] = static_cast<float>(acc[1]) * sk1;
-                    y[nb][2] = static_cast<float>(acc[2]) * sk0, y[nb][3] = static_cast<float>(acc[3]) * sk1;
+                    const uint32_t a = sc + (my_row[kk] + krow_n) * 4u;
+                    const float sk0 = lds_f(a), sk1 = lds_f(a + 32u);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        y[nb][2 * kk][0] = static_cast<float>(acc[nb][0]) * sk0;
+                        y[nb][2 * kk][1] = static_cast<float>(acc[nb][1]) * sk0;
+                        y[nb][2 * kk + 1][0] = static_cast<float>(acc[nb][2]) * sk1;
+                        y[nb][2 * kk + 1][1] = static_cast<float>(acc[nb][3]) * sk1;
+                    }
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int32_t j = j0 + 8 * nb + static_cast<int32_t>((i & 1) ? e ^ 4u : e);
-                            const bool see = j <= pos[i >> 1] && (j >= low[i >> 1] || j < p.sinks) &&
-                                             ((there >> my_box[nb >> 1]) & 1u) != 0u;
-                            y[nb][i] = see ? y[nb][i] : -INFINITY;
-                        }
+                        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int32_t j = j0 + 8 * kb + static_cast<int32_t>(krow_n);
+                                const bool see = j <= pos[nb][c] && (j >= low[nb][c] || j < p.sinks) &&
+                                                 ((there >> my_box[kb >> 1]) & 1u) != 0u;
+                                y[nb][kb][c] = see ? y[nb][kb][c] : -INFINITY;
+                            }
                 }
-                float alpha[2] = {1.0f, 1.0f};
+                // the sums are rescaled only when a row's maximum grows by more than 2^8
+                float mx[NB][2];
                 bool grew = false;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u == 1 && !two)
-                        break;
-                    float mx = fmaxf(max3f(y[0][2 * u], y[0][2 * u + 1], y[1][2 * u]),
-                                     max3f(y[1][2 * u + 1], y[2][2 * u], y[2][2 * u + 1]));
-                    mx = max3f(mx, y[3][2 * u], y[3][2 * u + 1]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float mb = mx * row_f[u];
-                    // the sums are rescaled only when the maximum grows by more than 2^8
-                    const bool grow = mb > m[u] + 8.0f;
-                    alpha[u] = grow ? ex2_approx(m[u] - mb) : 1.0f;
-                    m[u] = grow ? mb : m[u];
-                    grew |= grow;
-                }
-                if (__any_sync(0xffffffffu, grew)) {
-                    l[0] *= alpha[0];
-                    l[1] *= alpha[1];
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int j = 0; j < DB; ++j) {
-                        mul2(o[j][0], o[j][1], o[j][0], o[j][1], alpha[0], alpha[0]);
-                        mul2(o[j][2], o[j][3], o[j][2], o[j][3], alpha[1], alpha[1]);
+                    for (int c = 0; c < 2; ++c) {
+                        mx[nb][c] = fmaxf(max3f(y[nb][0][c], y[nb][1][c], y[nb][2][c]), y[nb][3][c]) * row_f[nb][c];
+                        grew |= mx[nb][c] > m[nb][c] + 8.0f;
+                    }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float alpha[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float mb = mx[nb][c];
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1)
+                                mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+                            const bool grow = mb > m[nb][c] + 8.0f;
+                            alpha[c] = grow ? ex2_approx(m[nb][c] - mb) : 1.0f;
+                            m[nb][c] = grow ? mb : m[nb][c];
+                            l[nb][c] *= alpha[c];
+                        }
+#pragma unroll
+                        for (int j = 0; j < DB; ++j) {
+                            mul2(o[nb][j][0], o[nb][j][1], o[nb][j][0], o[nb][j][1], alpha[0], alpha[1]);
+                            mul2(o[nb][j][2], o[nb][j][3], o[nb][j][2], o[nb][j][3], alpha[0], alpha[1]);
+                        }
                     }
                 }
-                uint32_t pa[4][2] = {};   // [nb][u]: probabilities times s_v, a bf16 pair
+                uint32_t pb[NB][4];   // probabilities times s_v: keys PI(2t), PI(2t + 1), query row g
                 auto weigh = [&](auto masked) {
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) {
-                        const uint32_t a = sc + (my_row[nb >> 1] + 8u * (nb & 1) + pp) * 4u;
-                        const float sv[2] = {lds_f(a + e * 4u), lds_f(a + (e ^ 4u) * 4u)};
+                    for (int kb = 0; kb < 4; ++kb) {
+                        const float sv = lds_f(sc + (my_row[kb >> 1] + 8u * (kb & 1) + pp + krow_n) * 4u);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            if (u == 1 && !two)
-                                break;
-                            const float neg_m = m[u] == -INFINITY ? 0.0f : -m[u];
+                        for (int nb = 0; nb < NB; ++nb) {
                             float pr[2];
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                const float x = ex2_approx(__fmaf_rn(y[nb][2 * u + c], row_f[u], neg_m));
-                                l[u] += x;
-                                pr[c] = x * sv[c];
+                                const float neg_m = m[nb][c] == -INFINITY ? 0.0f : -m[nb][c];
+                                const float x = ex2_approx(__fmaf_rn(y[nb][kb][c], row_f[nb][c], neg_m));
+                                l[nb][c] += x;
+                                pr[c] = x * sv;
                                 // a hidden key adds 0 whatever its scale holds
                                 if (decltype(masked)::value)
                                     pr[c] = x == 0.0f ? 0.0f : pr[c];
                             }
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
-                            pa[nb][u] = *reinterpret_cast<const uint32_t *>(&h2);
+                            pb[nb][kb] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h2));
                         }
                     }
                 };
@@ -763,28 +792,32 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                     weigh(PagedFlag<false>());
                 else
                     weigh(PagedFlag<true>());
-                // values of keys PI(2t), PI(2t+1) of two 8-key blocks, this lane's DB dims
+                // values of keys PI(2t), PI(2t + 1) of two 8-key blocks, this lane's D / 8 dims
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    uint32_t vb[4][DB / 4];
+                for (int kk = 0; kk < 2; ++kk) {
+                    uint32_t vb[4][D / 32];
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t kr = (kk & 1) ? e ^ 4u : e;
-                        const uint32_t row = codes[hb] + (pp + 8u * (kk >> 1) + kr) * D;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t kr = (i & 1) ? e ^ 4u : e;
+                        const uint32_t row = codes[kk] + (pp + 8u * (i >> 1) + kr) * D;
                         if (D == 128) {
                             const uint4 a = lds_u4(row + ((g ^ kr) << 4));
-                            vb[kk][0] = a.x, vb[kk][1] = a.y, vb[kk][DB / 4 - 2] = a.z, vb[kk][DB / 4 - 1] = a.w;
+                            vb[i][0] = a.x, vb[i][1] = a.y, vb[i][D / 32 - 2] = a.z, vb[i][D / 32 - 1] = a.w;
                         } else {
                             const uint32_t a = row + (((g >> 1) ^ (kr >> 1)) << 4) + (g & 1u) * 8u;
                             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                         : "=r"(vb[kk][0]), "=r"(vb[kk][1]) : "r"(a) : "memory");
+                                         : "=r"(vb[i][0]), "=r"(vb[i][1]) : "r"(a) : "memory");
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < DB; ++j) {
-                        const uint32_t b0 = codes_to_bf16x2(vb[0][j >> 2], vb[1][j >> 2], j & 3);
-                        const uint32_t b1 = codes_to_bf16x2(vb[2][j >> 2], vb[3][j >> 2], j & 3);
-                        mma_m16n8k16_bf16(o[j], pa[2 * hb][0], pa[2 * hb][1], pa[2 * hb + 1][0], pa[2 * hb + 1][1], b0, b1);
+                        uint32_t a[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = codes_to_bf16x2(vb[i & 2][j >> 1], vb[(i & 2) + 1][j >> 1], (2 * j + (i & 1)) & 3);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pb[nb][2 * kk], pb[nb][2 * kk + 1]);
                     }
                 }
             }
@@ -799,57 +832,59 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
         // ------------------------------------------------ join the four warps' sums
         // the maximum over the warps first; then one warp after the other adds its sums
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-            if (t == 0)
-                ml[warp * kFewRows + g + 8 * u] = make_float2(m[u], l[u]);
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+                    l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], x);
+                if (g == 0)
+                    ml[warp * ROWS + 8 * nb + 2 * t + c] = make_float2(m[nb][c], l[nb][c]);
+            }
         few_sync();
-        float scale_o[2];
+        float scale_o[NB][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float mm = -INFINITY;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mm = fmaxf(mm, ml[i * kFewRows + g + 8 * u].x);
-            scale_o[u] = m[u] == -INFINITY ? 0.0f : kCodeUnit * ex2_approx(m[u] - mm);
-        }
-        // lane (g, t): dims [2 DB t, 2 DB (t + 1)) of rows g and g + 8: o[j][0] is dim 2 DB t + j,
-        // o[j][1] dim 2 DB t + DB + j
+            for (int c = 0; c < 2; ++c) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mm = fmaxf(mm, ml[i * ROWS + 8 * nb + 2 * t + c].x);
+                scale_o[nb][c] = m[nb][c] == -INFINITY ? 0.0f : kCodeUnit * ex2_approx(m[nb][c] - mm);
+            }
+        // o[nb][j][c], o[nb][j][2 + c]: dims 2j, 2j + 1 of the lane's, query row 8 nb + 2t + c
 #pragma unroll 1
         for (uint32_t turn = 0; turn < 4; ++turn) {
             if (turn == warp) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u == 1 && !two)
-                        break;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int c = 0; c < 2 * DB / 4; ++c) {
-                        const int hb = c / (DB / 4), jj = (c % (DB / 4)) * 4;
-                        float4 *at = reinterpret_cast<float4 *>(obuf + (g + 8 * u) * C::O_LD + 2 * DB * t + 4 * c);
-                        float4 x = turn == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
-                        x.x = __fmaf_rn(o[jj][2 * u + hb], scale_o[u], x.x);
-                        x.y = __fmaf_rn(o[jj + 1][2 * u + hb], scale_o[u], x.y);
-                        x.z = __fmaf_rn(o[jj + 2][2 * u + hb], scale_o[u], x.z);
-                        x.w = __fmaf_rn(o[jj + 3][2 * u + hb], scale_o[u], x.w);
-                        *at = x;
-                    }
-                }
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < DB; j += 2) {
+                            float4 *at = reinterpret_cast<float4 *>(obuf + (8 * nb + 2 * t + c) * C::O_LD + 2 * DB * g + 2 * j);
+                            float4 x = turn == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
+                            x.x = __fmaf_rn(o[nb][j][c], scale_o[nb][c], x.x);
+                            x.y = __fmaf_rn(o[nb][j][2 + c], scale_o[nb][c], x.y);
+                            x.z = __fmaf_rn(o[nb][j + 1][c], scale_o[nb][c], x.z);
+                            x.w = __fmaf_rn(o[nb][j + 1][2 + c], scale_o[nb][c], x.w);
+                            *at = x;
+                        }
             }
             few_sync();
         }
         const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
-        float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * few_piece_floats<D>();
+        float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
 #pragma unroll 1
         for (int32_t lr = static_cast<int32_t>(warp); lr < rows; lr += 4) {
             float mm = -INFINITY, ll = 0.0f, v[E];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                mm = fmaxf(mm, ml[i * kFewRows + lr].x);
+                mm = fmaxf(mm, ml[i * ROWS + lr].x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 x = ml[i * kFewRows + lr];
+                const float2 x = ml[i * ROWS + lr];
                 ll = __fmaf_rn(x.y, x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mm), ll);
             }
 #pragma unroll
@@ -864,7 +899,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
                 for (int d = 0; d < E; ++d)
                     ws[lr * D + lane * E + d] = v[d];
                 if (lane == 0)
-                    *reinterpret_cast<float2 *>(ws + kFewRows * D + 2 * lr) = make_float2(mm, ll);
+                    *reinterpret_cast<float2 *>(ws + ROWS * D + 2 * lr) = make_float2(mm, ll);
             }
         }
         if (threadIdx.x == 0 && begins && !ends) {
@@ -877,7 +912,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewPerSm)
             desc->r0 = r0;
             piece_no = 1;
         }
-        walk_next_segment<kFewTile, kFewRows>(p, w);
+        walk_next_segment<kFewTile, ROWS>(p, w);
         few_sync();   // obuf, ml and the query codes are free again
     }
     if (threadIdx.x == 0 && piece_no == 0)

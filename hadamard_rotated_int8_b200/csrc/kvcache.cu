@@ -116,43 +116,56 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     return launch_status();
 }
 
-// The workspace of one call: what the blocks of the two kernels say of their last segment, then
-// the pieces of both (two a block).
-constexpr int64_t kPagedDescBytes = (static_cast<int64_t>(kFewPerSm) * kPagedMaxSms * sizeof(FewDesc) + 255) / 256 * 256;
+// The workspace of one call: what the blocks say of their last segment, then their pieces.
+constexpr int64_t kPagedDescBytes = (3ll * kPagedMaxSms * sizeof(FewDesc) + 255) / 256 * 256;
 
-template <int D>
-int64_t few_piece_bytes() { return 2ll * kFewPerSm * kPagedMaxSms * few_piece_floats<D>() * 4; }
+template <int D, int NB>
+constexpr int64_t few_piece_bytes()
+{
+    using C = FewConfig<D, NB>;
+    static_assert(C::PER_SM <= 3, "kPagedDescBytes");
+    return 2ll * C::PER_SM * kPagedMaxSms * C::PIECE * 4;
+}
 
 int64_t paged_workspace(int64_t D)
 {
-    return kPagedDescBytes + (D == 128 ? few_piece_bytes<128>() : few_piece_bytes<64>());
+    const int64_t one = D == 128 ? few_piece_bytes<128, 1>() : few_piece_bytes<64, 1>();
+    const int64_t two = D == 128 ? few_piece_bytes<128, 2>() : few_piece_bytes<64, 2>();
+    return kPagedDescBytes + (one > two ? one : two);
 }
 
-template <int D>
-sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, uint8_t *ws, cudaStream_t cs)
+template <int D, int NB>
+sdnq_status launch_few(const PagedParams &p, const DeviceInfo &dev, int sms, cudaStream_t cs)
 {
-    const int sms = dev.sm_count < kPagedMaxSms ? dev.sm_count : kPagedMaxSms;
+    using C = FewConfig<D, NB>;
     const uint32_t page = 1u << p.page_shift;
     const uint64_t pool_rows = static_cast<uint64_t>(p.pages > 0 ? p.pages : 1) * p.Hkv * 2 * page;
-    const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    CUtensorMap map_few;
-    if (!make_tmap_2d(&map_few, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D,
-                      page <= kFewBox ? 2 * page : kFewBox, swizzle))
+    CUtensorMap map;
+    if (!make_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D,
+                      page <= kFewBox ? 2 * page : kFewBox,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return SDNQ_ERR_CUDA;
-    static PerDeviceCache<1> smem_few;
-    if (!smem_attr_once(smem_few, dev.index, attn_few_kernel<D>, FewConfig<D>::SMEM_BYTES)) {
+    static PerDeviceCache<1> smem;
+    if (!smem_attr_once(smem, dev.index, attn_few_kernel<D, NB>, C::SMEM_BYTES)) {
         cudaGetLastError();
         return SDNQ_ERR_CUDA;
     }
+    const unsigned blocks = static_cast<unsigned>(C::PER_SM * sms);
+    launch_programmatic(attn_few_kernel<D, NB>, dim3(blocks), dim3(kFewThreads), C::SMEM_BYTES, cs, map, p);
+    launch_programmatic(attn_join_kernel<D, C::ROWS>, dim3(blocks, 2), dim3(kJoinThreads), 0, cs, p);
+    return launch_status();
+}
+
+template <int D>
+sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, int64_t max_q, uint8_t *ws, cudaStream_t cs)
+{
+    const int sms = dev.sm_count < kPagedMaxSms ? dev.sm_count : kPagedMaxSms;
     p.desc = ws;
     p.partial = reinterpret_cast<float *>(ws + kPagedDescBytes);
     p.rows_min = 0;
     p.rows_max = INT32_MAX;
     p.least_tiles = 2;
-    const unsigned blocks = static_cast<unsigned>(kFewPerSm * sms);
-    launch_programmatic(attn_few_kernel<D>, dim3(blocks), dim3(kFewThreads), FewConfig<D>::SMEM_BYTES, cs, map_few, p);
-    launch_programmatic(attn_join_kernel<D, kFewRows>, dim3(blocks, 2), dim3(kJoinThreads), 0, cs, p);
-    return launch_status();
+    return max_q <= 8 / p.share ? launch_few<D, 1>(p, dev, sms, cs) : launch_few<D, 2>(p, dev, sms, cs);
 }
 
 // Largest context, window and sink count that the kernels' 32-bit positions hold.
@@ -218,8 +231,8 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     cudaGetLastError();
     p.timeout_ns = kDefaultTimeoutNs;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return D == 128 ? launch_paged<128>(p, dev, static_cast<uint8_t *>(ws), cs)
-                    : launch_paged<64>(p, dev, static_cast<uint8_t *>(ws), cs);
+    return D == 128 ? launch_paged<128>(p, dev, max_q, static_cast<uint8_t *>(ws), cs)
+                    : launch_paged<64>(p, dev, max_q, static_cast<uint8_t *>(ws), cs);
 }
 
 } // namespace
