@@ -3,6 +3,7 @@
 // This file is part of libsdnq.cu's translation unit (included at its end).
 
 #include "attention_paged.cuh"
+#include "attention_paged_chunk.cuh"
 #include "kvcache.cuh"
 
 namespace sdnq {
@@ -116,34 +117,41 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     return launch_status();
 }
 
-// The workspace of one call: what the blocks say of their last segment, then their pieces.
-constexpr int64_t kPagedDescBytes = (3ll * kPagedMaxSms * sizeof(FewDesc) + 255) / 256 * 256;
+// The workspace of one call: what the blocks of each kernel say of their last segment, then the
+// few-row kernel's pieces, then the chunk kernel's.
+constexpr int64_t kPagedFewDescs = 3ll * kPagedMaxSms, kPagedChunkDescs = kPagedMaxSms;
+constexpr int64_t kPagedDescBytes = ((kPagedFewDescs + kPagedChunkDescs) * sizeof(FewDesc) + 255) / 256 * 256;
 
-template <int D, int NB>
-constexpr int64_t few_piece_bytes()
+template <int D>
+constexpr int64_t few_pieces_bytes()
 {
-    using C = FewConfig<D, NB>;
-    static_assert(C::PER_SM <= 3, "kPagedDescBytes");
-    return 2ll * C::PER_SM * kPagedMaxSms * C::PIECE * 4;
+    static_assert(FewConfig<D, 1>::PER_SM <= 3 && FewConfig<D, 2>::PER_SM <= 3, "kPagedFewDescs");
+    const int64_t one = FewConfig<D, 1>::PER_SM * FewConfig<D, 1>::PIECE, two = FewConfig<D, 2>::PER_SM * FewConfig<D, 2>::PIECE;
+    return (2ll * kPagedMaxSms * (one > two ? one : two) * 4 + 255) / 256 * 256;
 }
 
 int64_t paged_workspace(int64_t D)
 {
-    const int64_t one = D == 128 ? few_piece_bytes<128, 1>() : few_piece_bytes<64, 1>();
-    const int64_t two = D == 128 ? few_piece_bytes<128, 2>() : few_piece_bytes<64, 2>();
-    return kPagedDescBytes + (one > two ? one : two);
+    return kPagedDescBytes + (D == 128 ? few_pieces_bytes<128>() + 2ll * kPagedMaxSms * ChunkConfig<128>::PIECE * 4
+                                       : few_pieces_bytes<64>() + 2ll * kPagedMaxSms * ChunkConfig<64>::PIECE * 4);
+}
+
+// The pool as rows of D codes, boxes of `rows` of them.
+template <int D>
+bool make_pool_map(CUtensorMap *map, const PagedParams &p, uint32_t rows)
+{
+    const uint64_t pool_rows = static_cast<uint64_t>(p.pages > 0 ? p.pages : 1) * p.Hkv * 2 << p.page_shift;
+    return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D, rows,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 template <int D, int NB>
 sdnq_status launch_few(const PagedParams &p, const DeviceInfo &dev, int sms, cudaStream_t cs)
 {
     using C = FewConfig<D, NB>;
-    const uint32_t page = 1u << p.page_shift;
-    const uint64_t pool_rows = static_cast<uint64_t>(p.pages > 0 ? p.pages : 1) * p.Hkv * 2 * page;
     CUtensorMap map;
-    if (!make_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, D, pool_rows, D, D,
-                      page <= kFewBox ? 2 * page : kFewBox,
-                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    const uint32_t page = 1u << p.page_shift;
+    if (!make_pool_map<D>(&map, p, page <= kFewBox ? 2 * page : kFewBox))
         return SDNQ_ERR_CUDA;
     static PerDeviceCache<1> smem;
     if (!smem_attr_once(smem, dev.index, attn_few_kernel<D, NB>, C::SMEM_BYTES)) {
@@ -157,6 +165,34 @@ sdnq_status launch_few(const PagedParams &p, const DeviceInfo &dev, int sms, cud
 }
 
 template <int D>
+sdnq_status launch_chunk(const PagedParams &p, const DeviceInfo &dev, int sms, cudaStream_t cs)
+{
+    using C = ChunkConfig<D>;
+    CUtensorMap map;
+    const uint32_t page = 1u << p.page_shift;
+    if (!make_pool_map<D>(&map, p, page <= kChunkBox ? page : kChunkBox))
+        return SDNQ_ERR_CUDA;
+    static PerDeviceCache<1> smem, regs;
+    // the kernel's warpgroups hand registers over: it must have been compiled with the number
+    // that the split assumes, or its wait for them would not end
+    const bool fits = regs.get(dev.index, 0, [&] {
+        cudaFuncAttributes a = {};
+        return cudaFuncGetAttributes(&a, attn_chunk_kernel<D>) == cudaSuccess && a.numRegs == kChunkRegs ? 1 : -1;
+    }) == 1;
+    if (!fits || !smem_attr_once(smem, dev.index, attn_chunk_kernel<D>, C::SMEM_BYTES)) {
+        cudaGetLastError();
+        return SDNQ_ERR_CUDA;
+    }
+    const unsigned blocks = static_cast<unsigned>(sms);
+    launch_programmatic(attn_chunk_kernel<D>, dim3(blocks), dim3(kChunkThreads), C::SMEM_BYTES, cs, map, p);
+    launch_programmatic(attn_join_kernel<D, kChunkRows>, dim3(blocks, 16), dim3(kJoinThreads), 0, cs, p);
+    return launch_status();
+}
+
+// Query rows of a kv head above which a sequence goes to the tensor-memory kernel.
+constexpr int32_t kPagedFewRows = 32;
+
+template <int D>
 sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, int64_t max_q, uint8_t *ws, cudaStream_t cs)
 {
     const int sms = dev.sm_count < kPagedMaxSms ? dev.sm_count : kPagedMaxSms;
@@ -165,7 +201,20 @@ sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, int64_t max_q, ui
     p.rows_min = 0;
     p.rows_max = INT32_MAX;
     p.least_tiles = 2;
-    return max_q <= 8 / p.share ? launch_few<D, 1>(p, dev, sms, cs) : launch_few<D, 2>(p, dev, sms, cs);
+    if (max_q <= 8 / p.share)
+        return launch_few<D, 1>(p, dev, sms, cs);
+    if (max_q <= kPagedFewRows / p.share)
+        return launch_few<D, 2>(p, dev, sms, cs);
+    p.rows_max = kPagedFewRows;
+    const sdnq_status st = launch_few<D, 2>(p, dev, sms, cs);
+    if (st != SDNQ_OK)
+        return st;
+    p.rows_min = kPagedFewRows;
+    p.rows_max = INT32_MAX;
+    p.least_tiles = 1;
+    p.desc = ws + kPagedFewDescs * sizeof(FewDesc);
+    p.partial = reinterpret_cast<float *>(ws + kPagedDescBytes + few_pieces_bytes<D>());
+    return launch_chunk<D>(p, dev, sms, cs);
 }
 
 // Largest context, window and sink count that the kernels' 32-bit positions hold.
