@@ -43,7 +43,8 @@ struct ChunkConfig {
     static constexpr int B_OFF = K_OFF + NK * K_STAGE;
     static constexpr int V_OFF = B_OFF + NB * B_STAGE;
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 128 key scales, 128 value scales a stage
-    static constexpr int BAR_OFF = SC_OFF + NS * 1024;
+    static constexpr int QS_OFF = SC_OFF + NS * 1024;       // query scales
+    static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
     // full and empty of each ring, then per tile s_full, s_empty, p_full, pv_done, turn, q_full; drain
     static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 12 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
@@ -78,16 +79,84 @@ template <int D>
 __device__ __forceinline__ void thread_butterfly(float (&v)[D], int32_t g)
 {
 #pragma unroll
-    for (int h = 1; h < D; h <<= 1)
+    for (int i = 0; i < D; i += 2) {
+        const float a = v[i], b = v[i + 1];
+        v[i] = __fadd_rn(a, b);
+        v[i + 1] = __fsub_rn(a, b);
+    }
+#pragma unroll
+    for (int h = 2; h < D; h <<= 1)
         if (h < 8 || h < g) {
 #pragma unroll
-            for (int i = 0; i < D; ++i)
+            for (int i = 0; i < D; i += 2)
+                if ((i & h) == 0)
+                    bfly2(v[i], v[i + 1], v[i + h], v[i + h + 1]);
+        }
+}
+
+// Four query rows of D, 8 lanes each with D / 8 consecutive elements: rotated and quantized as
+// the row quantizer does it. Returns the codes, packed, and the row's scale.
+template <int D>
+__device__ __forceinline__ void quant_rows8(float (&v)[D / 8], int32_t g, float c_g, uint32_t lane,
+                                            uint32_t (&codes)[D / 32], float &s)
+{
+    constexpr int E = D / 8;
+#pragma unroll
+    for (int h = 1; h < E; h <<= 1)
+        if (h < 8 || h < g) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
                 if ((i & h) == 0) {
                     const float a = v[i], b = v[i + h];
                     v[i] = __fadd_rn(a, b);
                     v[i + h] = __fsub_rn(a, b);
                 }
         }
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1)
+        if (x * E < g) {
+            const float sgn = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                v[i] = __fmaf_rn(v[i], sgn, __shfl_xor_sync(0xffffffffu, v[i], x));
+        }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float s_z = __fdiv_rn(m, 127.0f);
+    const bool zero = !(m > 0.0f);
+    float s_q = s_z;
+    if (s_z < 0x1p-126f) {   // a subnormal step: the same quotients, 2^64 times as large on both sides
+        s_q = s_z * 0x1p64f;
+        const float most = s_q * 127.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            v[i] = fminf(fmaxf(v[i] * 0x1p64f, -most), most);
+    }
+    const float rcp = __frcp_rn(s_q);
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = v[8 * c + i];
+        const uint2 w = quant8(z, s_q, rcp, true);
+        codes[2 * c] = zero ? 0u : w.x;
+        codes[2 * c + 1] = zero ? 0u : w.y;
+    }
+    s = zero ? 0.0f : __fmul_rn(s_z, c_g);
+}
+
+// Bits [from, to) of the 32 that begin at bit `at`.
+__device__ __forceinline__ uint32_t bit_range(int32_t from, int32_t to, int32_t at)
+{
+    const int32_t a = min(max(from - at, 0), 32), b = min(max(to - at, 0), 32);
+    const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+    return below_b & ~below_a;
 }
 
 template <int D>
@@ -120,6 +189,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    float *qs = reinterpret_cast<float *>(smem + C::QS_OFF);
     const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
 
     if (threadIdx.x == 0) {
@@ -275,28 +345,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 constexpr uint32_t IDESC_S = idesc_s8_s32(128, 128);
                 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
                 uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
-                uint32_t s_n[2] = {0, 0}, p_n[2] = {0, 0}, pieces = 0;   // issued per tile
+                uint32_t s_n = 0, p_n = 0, pieces = 0;   // bit t: products of tile t issued so far, mod 2
                 int64_t n = 0;
                 bool ok = true;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
                     ok = ok && mbar_wait_bounded(bar, parity, abort, p.timeout_ns);
                     return ok;
                 };
+                // operand descriptors; 16 bytes further on is 1 more
+                const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
+                const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
                 // S_t = Q_t K^T of the next key tile, for the tiles in use
                 auto issue_s = [&](uint32_t in_use) {
                     if (!wait(k_full(ks), kph))
                         return;
+#pragma unroll 1
                     for (uint32_t t = 0; t < in_use; ++t) {
-                        if (!wait(s_empty(t), (s_n[t] & 1u) ^ 1u))
+                        if (!wait(s_empty(t), ((s_n >> t) & 1u) ^ 1u))
                             return;
                         tc_fence_after_sync();
-                        const uint32_t qa = base + C::Q_OFF + t * C::Q_TILE, ka = base + C::K_OFF + ks * C::K_STAGE;
+                        const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            mma_s8(tmem_base + t * 128, codes_desc<D>(qa + 32 * k), codes_desc<D>(ka + 32 * k), IDESC_S,
-                                   k != 0 ? 1u : 0u);
+                            mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
                         tc_commit(s_full(t));
-                        ++s_n[t];
+                        s_n ^= 1u << t;
                     }
                     tc_commit(k_empty(ks));
                     if (++ks == NK)
@@ -308,25 +381,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     wait(q_full(0), pieces & 1u);
                     wait(q_full(1), pieces & 1u);
                     ++pieces;
-                    if (ok)
-                        issue_s(in_use);
-                    for (int32_t k = 0; ok && k < tiles; ++k) {
+#pragma unroll 1
+                    for (int32_t k = -1; ok && k < tiles; ++k) {
                         if (k + 1 < tiles)
                             issue_s(in_use);
+                        if (k < 0)
+                            continue;
+#pragma unroll 1
                         for (uint32_t t = 0; ok && t < in_use; ++t) {
-                            if (!wait(p_full(t), p_n[t] & 1u))
+                            if (!wait(p_full(t), (p_n >> t) & 1u))
                                 break;
                             uint32_t slot = bs, ph = bph;
+#pragma unroll 1
                             for (uint32_t half = 0; half < 2; ++half) {
                                 if (!wait(b_full(slot), ph))
                                     break;
                                 tc_fence_after_sync();
-                                const uint32_t pa = base + C::P_OFF + t * C::P_TILE + half * 16384u;
-                                const uint32_t va = base + C::B_OFF + slot * C::B_STAGE;
+                                const uint64_t pa = dp + t * (C::P_TILE >> 4) + half * (16384u >> 4);
+                                const uint64_t va = db + slot * (C::B_STAGE >> 4);
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    mma_f16(tmem_base + 256 + t * 128, kmajor_desc(pa + 32 * kk),
-                                            mnmajor_desc(va + 2048 * kk, 8192), IDESC_PV,
+                                    mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV,
                                             (k | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
                                 if (t + 1 == in_use)
                                     tc_commit(b_empty(slot));
@@ -336,7 +411,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             if (!ok)
                                 break;
                             tc_commit(pv_done(t));
-                            ++p_n[t];
+                            p_n ^= 1u << t;
                             if (t + 1 == in_use)
                                 bs = slot, bph = ph;
                         }
@@ -360,7 +435,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!ok)
                     break;
                 const uint32_t src = base + C::V_OFF + vs * C::V_STAGE, dst = base + C::B_OFF + bs * C::B_STAGE;
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < 4 * D / 64; ++i) {
                     const uint32_t idx = i * 64u + me, key = idx / (D / 16), c = idx % (D / 16);   // 16 dims of a key
                     const uint32_t at = D == 128 ? key * 128u + ((c ^ (key & 7u)) << 4)
@@ -407,13 +482,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int32_t tiles = piece_tiles(n), rows = piece_rows(), r0 = w.q * kChunkRows;
             const bool active = static_cast<int32_t>(tile) * 128 < rows;
             const int32_t tok = (r0 + min(lr, rows - 1)) / p.share;
-            const int32_t head = w.kvh * p.share + r0 + min(lr, rows - 1) - tok * p.share;
             const int32_t pos0 = w.s.len - w.s.n;
-            const int32_t pos = pos0 + tok, low = p.window > 0 ? pos - p.window + 1 : INT32_MIN;
+            const int32_t pos = pos0 + tok, low = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
             // the tile's first and last row: which key tiles are wholly visible
             const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
             const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
-            const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : INT32_MIN;
+            const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
             if (!active) {   // no row in this tile: only its part in the handshakes
                 __syncwarp();
                 if (lane == 0)
@@ -435,60 +509,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
             }
-            float row_f;
+            // this warp's 32 query rows, four at a time: rotated, quantized, into the operand
+            // tile; the next four's elements are on their way meanwhile
             {
-                // the query row: rotated, quantized, into the operand tile
-                float v[D];
-                const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + tok) * p.ldq + static_cast<int64_t>(head) * D;
+                constexpr int E = D / 8, V = D / 64;   // elements and 16-byte vectors of a lane
+                auto load = [&](int32_t it, uint4 (&x)[V]) {
+                    const int32_t row = static_cast<int32_t>(tile) * 128 + static_cast<int32_t>(quad) * 32 + it * 4 + static_cast<int32_t>(lane >> 3);
+                    const int32_t tk = (r0 + row) / p.share;
+                    const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + tk) * p.ldq +
+                                        static_cast<int64_t>(w.kvh * p.share + r0 + row - tk * p.share) * D + (lane & 7u) * E;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 a = lr < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+                    for (int i = 0; i < V; ++i)
+                        x[i] = it < 8 && row < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                };
+                uint4 x[V], x_next[V];
+                load(0, x);
+#pragma unroll 1
+                for (int32_t it = 0; it < 8; ++it) {
+                    load(it + 1, x_next);
+                    float v[E];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        v[8 * i + 2 * u] = __uint_as_float(x[u] << 16);
-                        v[8 * i + 2 * u + 1] = __uint_as_float(x[u] & 0xffff0000u);
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t b[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            v[8 * i + 2 * u] = __uint_as_float(b[u] << 16);
+                            v[8 * i + 2 * u + 1] = __uint_as_float(b[u] & 0xffff0000u);
+                        }
+                        x[i] = x_next[i];
                     }
+                    uint32_t codes[D / 32];
+                    float sq;
+                    quant_rows8<D>(v, p.group, p.c_g, lane, codes, sq);
+                    const uint32_t row = quad * 32u + it * 4u + (lane >> 3), c = lane & 7u;
+                    const uint32_t at = base + C::Q_OFF + tile * C::Q_TILE + row * D;
+                    if (D == 128)
+                        sts_v4(at + ((c ^ (row & 7u)) << 4), codes[0], codes[1], codes[D / 32 - 2], codes[D / 32 - 1]);
+                    else
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (((c >> 1) ^ ((row >> 1) & 3u)) << 4) + (c & 1u) * 8u),
+                                     "r"(codes[0]), "r"(codes[1])
+                                     : "memory");
+                    if (c == 0u)
+                        qs[tile * 128u + row] = sq;
                 }
-                thread_butterfly<D>(v, p.group);
-                float m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < D; ++i)
-                    m = fmaxf(m, fabsf(v[i]));
-                const float s_z = __fdiv_rn(m, 127.0f);
-                const bool zero = !(m > 0.0f);
-                float s_q = s_z;
-                if (s_z < 0x1p-126f) {   // a subnormal step: the same quotients, 2^64 times as large on both sides
-                    s_q = s_z * 0x1p64f;
-                    const float most = s_q * 127.0f;
-#pragma unroll
-                    for (int i = 0; i < D; ++i)
-                        v[i] = fminf(fmaxf(v[i] * 0x1p64f, -most), most);
-                }
-                const float rcp = __frcp_rn(s_q);
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint2 a = make_uint2(0u, 0u), b = make_uint2(0u, 0u);
-                    if (!zero) {
-                        float z[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            z[i] = v[16 * c + i];
-                        a = quant8(z, s_q, rcp, true);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            z[i] = v[16 * c + 8 + i];
-                        b = quant8(z, s_q, rcp, true);
-                    }
-                    const uint32_t sw = D == 128 ? static_cast<uint32_t>(c) ^ (r & 7) : static_cast<uint32_t>(c) ^ ((r >> 1) & 3);
-                    sts_v4(base + C::Q_OFF + tile * C::Q_TILE + r * D + (sw << 4), a.x, a.y, b.x, b.y);
-                }
-                // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
-                const float sq = zero ? 0.0f : __fmul_rn(s_z, p.c_g);
-                row_f = fmaxf(sq * p.scale * 1.4426950408889634f, 0x1p-126f);
                 fence_proxy_async_smem();
             }
             __syncwarp();
+            // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
+            const float row_f = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
             if (lane == 0)
                 mbar_arrive(q_full(tile));
             float m_used = -INFINITY, l_sum = 0.0f;
@@ -499,65 +567,64 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok)
                     break;
-                float y[128];
-                float alpha = 1.0f;
-                bool any_grow = false, whole = true;
                 tc_fence_after_sync();
-                // fp32(acc) without the conversion pipe (attention.cuh)
-                {
-                    uint32_t a[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld_32x32b_x32(t_lane + s_col + c * 32, a[c]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            y[c * 32 + i] = __uint_as_float(a[c][i] + 0x4B400000u);
-                }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(s_empty(tile));
-                const uint32_t skb = base + C::SC_OFF + ss * 1024u;
-#pragma unroll
-                for (int c4 = 0; c4 < 32; ++c4) {
-                    const float4 k4 = lds_v4(skb + c4 * 16u);   // a broadcast
-                    float f0, f1, f2, f3;
-                    sub2(f0, f1, y[4 * c4], y[4 * c4 + 1], 12582912.0f, 12582912.0f);
-                    sub2(f2, f3, y[4 * c4 + 2], y[4 * c4 + 3], 12582912.0f, 12582912.0f);
-                    mul2(y[4 * c4], y[4 * c4 + 1], f0, f1, k4.x, k4.y);          // acc * s_k
-                    mul2(y[4 * c4 + 2], y[4 * c4 + 3], f2, f3, k4.z, k4.w);
-                }
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
                 const uint32_t there = meta[ss];
-                whole = j0 + 127 <= pos_first && (j0 >= low_last || j0 + 128 <= p.sinks) && there == all_boxes;
-                if (!whole) {
-                    // visible columns: [from, to) and those of the sinks, in pages that are there
-                    uint32_t there16 = 0;   // a bit for each 16 columns
+                const bool whole = j0 + 127 <= pos_first && (j0 >= low_last || j0 + 128 <= p.sinks) && there == all_boxes;
+                // visible columns of the 32 from c on: [low, pos] and the sinks, in pages that are there
+                auto visible = [&](int32_t c) {
+                    uint32_t in = 0;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        there16 |= ((there >> ((c * 16) >> pp_shift)) & 1u) << c;
-                    const int32_t to = pos - j0 + 1, from = low > j0 - 128 ? low - j0 : -128, sink = p.sinks - j0;
+                    for (int u = 0; u < 2; ++u)
+                        in |= ((there >> ((c + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
+                    return in & (bit_range(low, pos + 1, j0 + c) | bit_range(0, min(p.sinks, pos + 1), j0 + c));
+                };
+                // The logits stay in TMEM, not in registers, between the two passes over them
+                // (loops of 64 columns): a row of 128 unrolled twice over overflowed the
+                // instruction cache, at 5 cycles an instruction.
+                const uint32_t skb = base + C::SC_OFF + ss * 1024u;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int32_t c = 0; c < 128; c += 64) {
+                    uint32_t a[2][32];
+                    tmem_ld_32x32b_x32(t_lane + s_col + c, a[0]);
+                    tmem_ld_32x32b_x32(t_lane + s_col + c + 32, a[1]);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) {
-                        const bool see = c < to && (c >= from || c < sink) && ((there16 >> (c / 16)) & 1u) != 0u;
-                        y[c] = see ? y[c] : -INFINITY;
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 k4 = lds_v4(skb + (c + h * 32 + e) * 4);   // a broadcast
+                            // fp32(acc) without the conversion pipe (attention.cuh), times s_k
+                            float f[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                f[u] = __uint_as_float(a[h][e + u] + 0x4B400000u);
+                            sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
+                            sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
+                            mul2(f[0], f[1], f[0], f[1], k4.x, k4.y);
+                            mul2(f[2], f[3], f[2], f[3], k4.z, k4.w);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                a[h][e + u] = __float_as_uint(f[u]);
+                        }
+                        if (!whole) {
+                            const uint32_t see = visible(c + h * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                a[h][e] = (see >> e) & 1u ? a[h][e] : 0xff800000u;   // -inf
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                mx[u] = max3f(mx[u], __uint_as_float(a[h][e + u]), __uint_as_float(a[h][e + u + 4]));
+                        tmem_st_32x32b_x32(t_lane + s_col + c + h * 32, a[h]);
                     }
                 }
-                // 4 independent chains, chain i over the columns i + 4k (k = 0..31)
-                float mx[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx[c] = y[c];
-#pragma unroll
-                    for (int u = 1; u + 1 < 32; u += 2)
-                        mx[c] = max3f(mx[c], y[c + 4 * u], y[c + 4 * u + 4]);
-                    mx[c] = fmaxf(mx[c], y[c + 124]);
-                }
                 const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
+                tmem_st_wait();
                 // the P tile is free, and O stable, once the tile's last product is done
                 if (k > 0) {
                     got = mbar_wait_bounded(pv_done(tile), (mine & 1u) ^ 1u, abort, p.timeout_ns);
@@ -567,7 +634,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     tc_fence_after_sync();
                 }
                 const bool grow = mb > m_used + 8.0f;
-                any_grow = __any_sync(0xffffffffu, grow);
+                const bool any_grow = __any_sync(0xffffffffu, grow);
+                float alpha = 1.0f;
                 if (any_grow) {
                     alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
                     m_used = grow ? mb : m_used;
@@ -579,45 +647,62 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok)
                     break;
-                const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + static_cast<uint32_t>(r) * 128u;
-                const uint32_t svb = base + C::SC_OFF + ss * 1024u + 512u;
-                const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
-                float ls[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // 8 independent partial sums
                 // P = 2^(y - m) s_v, bf16, into the swizzled K-major tile (attention.cuh)
-                auto weigh = [&](auto masked) {
-#pragma unroll
-                    for (int ch = 0; ch < 16; ++ch) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int e2 = 0; e2 < 2; ++e2) {
-                            const float4 v4 = lds_v4(svb + ch * 32u + e2 * 16u);
-                            const float sv[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int c = ch * 8 + e2 * 4 + 2 * e;
-                                float d0, d1, w0, w1;
-                                fma2(d0, d1, y[c], y[c + 1], row_f, row_f, neg_m, neg_m);
-                                const float p0 = ex2_approx(d0), p1 = ex2_approx(d1);
-                                float &l0 = ls[4 * e2 + 2 * e], &l1 = ls[4 * e2 + 2 * e + 1];
-                                add2(l0, l1, l0, l1, p0, p1);
-                                mul2(w0, w1, p0, p1, sv[2 * e], sv[2 * e + 1]);
-                                if (decltype(masked)::value) {   // a hidden key adds 0 whatever its scale holds
-                                    w0 = p0 == 0.0f ? 0.0f : w0;
-                                    w1 = p1 == 0.0f ? 0.0f : w1;
-                                }
-                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(w0, w1);
-                                x[2 * e2 + e] = *reinterpret_cast<const uint32_t *>(&h2);
-                            }
-                        }
-                        const uint32_t c16 = static_cast<uint32_t>(ch & 7) ^ (static_cast<uint32_t>(r) & 7u);
-                        sts_v4(prow + static_cast<uint32_t>(ch >> 3) * 16384u + (c16 << 4), x[0], x[1], x[2], x[3]);
+                const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + static_cast<uint32_t>(r) * 128u;
+                const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
+                float ls[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                for (int32_t c = 0; c < 128; c += 64) {
+                    uint32_t a[2][32];
+                    tmem_ld_32x32b_x32(t_lane + s_col + c, a[0]);
+                    tmem_ld_32x32b_x32(t_lane + s_col + c + 32, a[1]);
+                    tmem_ld_wait();
+                    if (c == 64) {   // the logits are read: S may be overwritten
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(s_empty(tile));
                     }
-                };
-                if (whole)
-                    weigh(PagedFlag<false>());
-                else
-                    weigh(PagedFlag<true>());
-                l_sum += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 v4 = lds_v4(skb + 512u + (c + h * 32 + e) * 4);
+                            float f[4];
+                            fma2(f[0], f[1], __uint_as_float(a[h][e]), __uint_as_float(a[h][e + 1]), row_f, row_f, neg_m, neg_m);
+                            fma2(f[2], f[3], __uint_as_float(a[h][e + 2]), __uint_as_float(a[h][e + 3]), row_f, row_f, neg_m, neg_m);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                f[u] = ex2_approx(f[u]);
+                            add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
+                            add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
+                            mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
+                            mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                a[h][e + u] = __float_as_uint(f[u]);
+                        }
+                        if (!whole) {   // a hidden key adds 0 whatever its scale holds
+                            const uint32_t see = visible(c + h * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                a[h][e] = (see >> e) & 1u ? a[h][e] : 0u;
+                        }
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[h][8 * ch + 2 * u]),
+                                                                                __uint_as_float(a[h][8 * ch + 2 * u + 1]));
+                                x[u] = *reinterpret_cast<const uint32_t *>(&h2);
+                            }
+                            const uint32_t c16 = static_cast<uint32_t>(h * 4 + ch) ^ (static_cast<uint32_t>(r) & 7u);
+                            sts_v4(prow + static_cast<uint32_t>(c >> 6) * 16384u + (c16 << 4), x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                }
+                l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(turn(tile ^ 1u));
@@ -665,6 +750,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (begins && ends) {
                         thread_butterfly<D>(v, p.group);
                         const float inv = l_sum == 0.0f ? 0.0f : __fdiv_rn(kCodeUnit * p.c_g, l_sum);
+                        const int32_t head = w.kvh * p.share + r0 + lr - tok * p.share;   // (of a row in use)
                         uint16_t *o = p.o + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(head) * D;
                         if (lr < rows) {
 #pragma unroll
