@@ -11,7 +11,7 @@
 // - warps 4..7 (tile 0) and 8..11 (tile 1), one thread a query row, rotate and quantize their
 //   query rows into the operand tile, then per key tile form base-2 logits, an online softmax
 //   (sums rescaled only when the maximum grows by more than 2^8), and P = probability * s_v in
-//   bf16. The tiles take turns at the exponentials. At the end of a segment the thread has its
+//   bf16. At the end of a segment the thread has its
 //   output row in registers: the rotation is undone there.
 // Bound: the exponentials. Per 256 x 128 tile the SM's 16 exponentials a cycle take 2048
 // cycles, the instructions of softmax and conversion about 1900 issue cycles a scheduler, the
@@ -45,8 +45,8 @@ struct ChunkConfig {
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 128 key scales, 128 value scales a stage
     static constexpr int QS_OFF = SC_OFF + NS * 1024;       // query scales
     static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
-    // full and empty of each ring, then per tile s_full, s_empty, p_full, pv_done, turn, q_full; drain
-    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 12 + 1;
+    // full and empty of each ring, then per tile s_full, p_full, pv_done, q_full; drain
+    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 8 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
     static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
@@ -180,12 +180,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto sc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + NS + s); };
     constexpr int TB = 2 * (NK + NV + NB + NS);
     auto s_full = [&](uint32_t t) { return bar0 + 8u * (TB + t); };
-    auto s_empty = [&](uint32_t t) { return bar0 + 8u * (TB + 2 + t); };
-    auto p_full = [&](uint32_t t) { return bar0 + 8u * (TB + 4 + t); };
-    auto pv_done = [&](uint32_t t) { return bar0 + 8u * (TB + 6 + t); };
-    auto turn = [&](uint32_t t) { return bar0 + 8u * (TB + 8 + t); };
-    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 10 + t); };
-    const uint32_t drain_bar = bar0 + 8u * (TB + 12);
+    auto p_full = [&](uint32_t t) { return bar0 + 8u * (TB + 2 + t); };
+    auto pv_done = [&](uint32_t t) { return bar0 + 8u * (TB + 4 + t); };
+    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 6 + t); };
+    const uint32_t drain_bar = bar0 + 8u * (TB + 8);
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -202,9 +200,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int s = 0; s < NS; ++s)
             mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 8);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1), mbar_init(s_empty(t), 4);
+            mbar_init(s_full(t), 1), mbar_init(q_full(t), 4);
             mbar_init(p_full(t), 4), mbar_init(pv_done(t), 1);
-            mbar_init(turn(t), 4), mbar_init(q_full(t), 4);
         }
         mbar_init(drain_bar, 1);
         *abort = 0;
@@ -345,7 +342,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 constexpr uint32_t IDESC_S = idesc_s8_s32(128, 128);
                 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
                 uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
-                uint32_t s_n = 0, p_n = 0, pieces = 0;   // bit t: products of tile t issued so far, mod 2
+                uint32_t q_n = 0, p_n = 0;   // bit t: pieces, and products with V, of tile t so far, mod 2
                 int64_t n = 0;
                 bool ok = true;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -355,42 +352,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // operand descriptors; 16 bytes further on is 1 more
                 const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
                 const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
-                // S_t = Q_t K^T of the next key tile, for the tiles in use
-                auto issue_s = [&](uint32_t in_use) {
-                    if (!wait(k_full(ks), kph))
-                        return;
-#pragma unroll 1
-                    for (uint32_t t = 0; t < in_use; ++t) {
-                        if (!wait(s_empty(t), ((s_n >> t) & 1u) ^ 1u))
-                            return;
-                        tc_fence_after_sync();
-                        const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
+                // S_t = Q_t K^T of the key tile in slot ks; the last tile's frees the slot
+                auto issue_s = [&](uint32_t t, bool last) {
+                    tc_fence_after_sync();
+                    const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
 #pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
-                        tc_commit(s_full(t));
-                        s_n ^= 1u << t;
+                    for (int k = 0; k < D / 32; ++k)
+                        mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
+                    tc_commit(s_full(t));
+                    if (last) {
+                        tc_commit(k_empty(ks));
+                        if (++ks == NK)
+                            ks = 0, kph ^= 1u;
                     }
-                    tc_commit(k_empty(ks));
-                    if (++ks == NK)
-                        ks = 0, kph ^= 1u;
                 };
                 while (ok && n < count) {
                     const int32_t tiles = piece_tiles(n);
                     const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
-                    wait(q_full(0), pieces & 1u);
-                    wait(q_full(1), pieces & 1u);
-                    ++pieces;
+                    // key tile k's S_t is issued when P_t of the one before is written (S_t has
+                    // been read then), and before that one's product with V, so that the tile's
+                    // softmax goes on while the product runs
 #pragma unroll 1
-                    for (int32_t k = -1; ok && k < tiles; ++k) {
-                        if (k + 1 < tiles)
-                            issue_s(in_use);
-                        if (k < 0)
-                            continue;
+                    for (int32_t k = 0; ok && k <= tiles; ++k) {
+                        if (k < tiles)
+                            wait(k_full(ks), kph);
 #pragma unroll 1
                         for (uint32_t t = 0; ok && t < in_use; ++t) {
-                            if (!wait(p_full(t), (p_n >> t) & 1u))
+                            if (k == 0 ? !wait(q_full(t), (q_n >> t) & 1u) : !wait(p_full(t), (p_n >> t) & 1u))
                                 break;
+                            if (k < tiles)
+                                issue_s(t, t + 1 == in_use);
+                            if (k == 0) {
+                                q_n ^= 1u << t;
+                                continue;
+                            }
                             uint32_t slot = bs, ph = bph;
 #pragma unroll 1
                             for (uint32_t half = 0; half < 2; ++half) {
@@ -402,7 +397,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
                                     mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV,
-                                            (k | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
+                                            ((k - 1) | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
                                 if (t + 1 == in_use)
                                     tc_commit(b_empty(slot));
                                 if (++slot == NB)
@@ -475,7 +470,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int32_t lr = static_cast<int32_t>(tile) * 128 + r;          // row of the segment's tile
         const uint32_t t_lane = tmem_base + ((quad * 32u) << 16);
         const uint32_t s_col = tile * 128u, o_col = 256u + tile * 128u;
-        uint32_t ss = 0, sph = 0, blocks = 0, mine = 0;   // scale ring; key tiles seen, and worked on
+        uint32_t ss = 0, sph = 0, mine = 0;   // scale ring; key tiles worked on
         bool ok = true, open = false;
         int64_t n = 0;
         while (ok && n < count) {
@@ -488,20 +483,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
             const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
             const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
-            if (!active) {   // no row in this tile: only its part in the handshakes
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(q_full(tile));
-                for (int32_t k = 0; k < tiles; ++k, ++blocks) {
-                    const bool got = mbar_wait_bounded(sc_full(ss), sph, abort, p.timeout_ns) &&
-                                     mbar_wait_bounded(turn(tile), tile == 0 ? (blocks & 1u) ^ 1u : blocks & 1u, abort, p.timeout_ns);
-                    ok = __all_sync(0xffffffffu, got);
+            if (!active) {   // no row in this tile: it only hands the scales on
+                for (int32_t k = 0; k < tiles; ++k) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sc_full(ss), sph, abort, p.timeout_ns));
                     if (!ok)
                         break;
-                    if (lane == 0) {
-                        mbar_arrive(turn(tile ^ 1u));
+                    if (lane == 0)
                         mbar_arrive(sc_empty(ss));
-                    }
                     if (++ss == NS)
                         ss = 0, sph ^= 1u;
                 }
@@ -561,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 mbar_arrive(q_full(tile));
             float m_used = -INFINITY, l_sum = 0.0f;
 #pragma unroll 1
-            for (int32_t k = 0; k < tiles; ++k, ++blocks) {
+            for (int32_t k = 0; k < tiles; ++k) {
                 bool got = mbar_wait_bounded(s_full(tile), mine & 1u, abort, p.timeout_ns) &&
                            mbar_wait_bounded(sc_full(ss), sph, abort, p.timeout_ns);
                 ok = __all_sync(0xffffffffu, got);
@@ -641,12 +629,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
                 }
-                // tile 0 runs its exponentials of a key tile after tile 1 ran those of the one
-                // before, tile 1 after tile 0 ran those of the same one
-                got = mbar_wait_bounded(turn(tile), tile == 0 ? (blocks & 1u) ^ 1u : blocks & 1u, abort, p.timeout_ns);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok)
-                    break;
                 // P = 2^(y - m) s_v, bf16, into the swizzled K-major tile (attention.cuh)
                 const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + static_cast<uint32_t>(r) * 128u;
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
@@ -657,12 +639,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     tmem_ld_32x32b_x32(t_lane + s_col + c, a[0]);
                     tmem_ld_32x32b_x32(t_lane + s_col + c + 32, a[1]);
                     tmem_ld_wait();
-                    if (c == 64) {   // the logits are read: S may be overwritten
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(s_empty(tile));
-                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -704,10 +680,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(turn(tile ^ 1u));
+                if (lane == 0)
                     mbar_arrive(sc_empty(ss));
-                }
                 if (++ss == NS)
                     ss = 0, sph ^= 1u;
                 if (any_grow && k > 0) {
