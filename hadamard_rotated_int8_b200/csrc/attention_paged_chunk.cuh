@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issue
-            if (lane == 0) {
+            // the whole warp walks the loops, so that descriptors stay in uniform registers; one
+            // lane issues
+            {
+                const bool leader = lane == 0;
                 constexpr uint32_t IDESC_S = idesc_s8_s32(128, 128);
                 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
                 uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 int64_t n = 0;
                 bool ok = true;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
-                    ok = ok && mbar_wait_bounded(bar, parity, abort, p.timeout_ns);
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, p.timeout_ns));
                     return ok;
                 };
                 // operand descriptors; 16 bytes further on is 1 more
@@ -356,12 +359,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 auto issue_s = [&](uint32_t t, bool last) {
                     tc_fence_after_sync();
                     const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
-                    tc_commit(s_full(t));
+                        for (int k = 0; k < D / 32; ++k)
+                            mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
+                        tc_commit(s_full(t));
+                        if (last)
+                            tc_commit(k_empty(ks));
+                    }
+                    __syncwarp();
                     if (last) {
-                        tc_commit(k_empty(ks));
                         if (++ks == NK)
                             ks = 0, kph ^= 1u;
                     }
@@ -394,18 +401,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                 tc_fence_after_sync();
                                 const uint64_t pa = dp + t * (C::P_TILE >> 4) + half * (16384u >> 4);
                                 const uint64_t va = db + slot * (C::B_STAGE >> 4);
+                                if (leader) {
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV,
-                                            ((k - 1) | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
-                                if (t + 1 == in_use)
-                                    tc_commit(b_empty(slot));
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV,
+                                                ((k - 1) | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
+                                    if (t + 1 == in_use)
+                                        tc_commit(b_empty(slot));
+                                    if (half == 1)
+                                        tc_commit(pv_done(t));
+                                }
+                                __syncwarp();
                                 if (++slot == NB)
                                     slot = 0, ph ^= 1u;
                             }
                             if (!ok)
                                 break;
-                            tc_commit(pv_done(t));
                             p_n ^= 1u << t;
                             if (t + 1 == in_use)
                                 bs = slot, bph = ph;
@@ -414,9 +425,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     n += tiles;
                     walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 }
-                tc_commit(drain_bar);
-                volatile int no_abort = 0;
-                mbar_wait_bounded(drain_bar, 0u, &no_abort, p.timeout_ns);
+                if (leader) {
+                    tc_commit(drain_bar);
+                    volatile int no_abort = 0;
+                    mbar_wait_bounded(drain_bar, 0u, &no_abort, p.timeout_ns);
+                }
             }
         } else {
             // -------------------------------------------------------- value codes to bf16
