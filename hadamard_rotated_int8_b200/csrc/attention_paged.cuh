@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
     const int64_t count = min(first + per, total) - first;
     const int32_t pp = min(1 << p.page_shift, kFewBox);         // keys of a box
     const int32_t pp_shift = min(p.page_shift, 6);
-    const int32_t nbox = kFewTile >> pp_shift;
+    const int32_t nbox = kFewTile >> pp_shift, nbox_shift = 7 - pp_shift;
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
@@ -513,10 +513,10 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
             // e % nbox of the piece's tile e / nbox.
             auto fetch = [&](int32_t e0) {
                 const int32_t e = e0 + static_cast<int32_t>(lane);
-                const int32_t i = w.i + e / nbox;
+                const int32_t i = w.i + (e >> nbox_shift);
                 if (i >= w.i + tiles)
                     return -1;
-                const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kFewTile + (e % nbox) * pp;
+                const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kFewTile + ((e & (nbox - 1)) << pp_shift);
                 if (j >= w.s.len)
                     return -1;
                 const int32_t id = row[j >> p.page_shift];
@@ -919,14 +919,15 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
         desc->pieces = 0;
 }
 
-// Joins the pieces of the segments that several blocks share: block (c, y) takes rows y, y +
-// gridDim.y, ... of the segment that begins in block c. Eight warps take the pieces in turn.
+// Joins the pieces of the segments that several blocks share: block (c, y) takes rows of the
+// segment that begins in block c. The block's eight warps take the pieces of one row in turn
+// (few rows, up to a whole grid of pieces), or a row each (ROWS > 16: many rows, few pieces).
 constexpr int kJoinThreads = 256;
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedParams p)
 {
-    constexpr int E = D / 32, W = kJoinThreads / 32;
+    constexpr int E = D / 32, W = ROWS > 16 ? 1 : kJoinThreads / 32;   // warps of a row
     constexpr int64_t PIECE = ROWS * (D + 2);
     __shared__ float part[W][D];
     __shared__ float2 part_ml[W];
@@ -937,13 +938,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedPara
     const uint32_t lane = lane_id();
     if (d.pieces == 0)
         return;
-    for (int32_t lr = blockIdx.y; lr < d.rows; lr += static_cast<int32_t>(gridDim.y)) {
+    const int32_t step = static_cast<int32_t>(gridDim.y) * (W == 1 ? kJoinThreads / 32 : 1);
+    for (int32_t lr = W == 1 ? static_cast<int32_t>(blockIdx.y) * (kJoinThreads / 32) + warp : static_cast<int32_t>(blockIdx.y);
+         lr < d.rows; lr += step) {
         float m = -INFINITY, l = 0.0f, v[E];
 #pragma unroll
         for (int i = 0; i < E; ++i)
             v[i] = 0.0f;
 #pragma unroll 4
-        for (int32_t k = warp; k < d.pieces; k += W) {
+        for (int32_t k = W == 1 ? 0 : warp; k < d.pieces; k += W) {
             const float *ws = p.partial + ((static_cast<int64_t>(blockIdx.x) + k) * 2 + (k == 0 ? 1 : 0)) * PIECE;
             const float2 x = *reinterpret_cast<const float2 *>(ws + ROWS * D + 2 * lr);
             float a[E];
@@ -959,11 +962,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedPara
                 v[i] = __fmaf_rn(a[i], fn, v[i] * fo);
             m = mn;
         }
+        const int32_t r = d.r0 + lr, tok = r / p.share;
+        if (W == 1) {
+            paged_store_row<D>(p, v, l, d.q0 + tok, d.head0 + r - tok * p.share, lane);
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            part[warp][lane * E + i] = v[i];
+            part[warp % W][lane * E + i] = v[i];
         if (lane == 0)
-            part_ml[warp] = make_float2(m, l);
+            part_ml[warp % W] = make_float2(m, l);
         __syncthreads();
         if (warp == 0) {
             float mm = -INFINITY, ll = 0.0f;
@@ -981,7 +989,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedPara
                 for (int i = 0; i < E; ++i)
                     v[i] = __fmaf_rn(part[k][lane * E + i], f, v[i]);
             }
-            const int32_t r = d.r0 + lr, tok = r / p.share;
             paged_store_row<D>(p, v, ll, d.q0 + tok, d.head0 + r - tok * p.share, lane);
         }
         __syncthreads();

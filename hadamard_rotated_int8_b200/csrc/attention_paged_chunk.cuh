@@ -27,10 +27,7 @@ namespace sdnq {
 constexpr int kChunkTile = 128;     // keys per step
 constexpr int kChunkRows = 256;     // query rows of a segment: two tiles of 128
 constexpr int kChunkBox = 64;       // keys of a box at most
-constexpr int kChunkThreads = 384;
-constexpr int kChunkRegs = 168;     // registers a thread at launch; see the split below
-constexpr int kChunkRegsLow = 72, kChunkRegsHigh = 216;
-static_assert(kChunkRegsLow + 2 * kChunkRegsHigh == 3 * kChunkRegs, "registers of the three warpgroups");
+constexpr int kChunkThreads = 640;
 
 template <int D>
 struct ChunkConfig {
@@ -44,18 +41,16 @@ struct ChunkConfig {
     static constexpr int V_OFF = B_OFF + NB * B_STAGE;
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 128 key scales, 128 value scales a stage
     static constexpr int QS_OFF = SC_OFF + NS * 1024;       // query scales
-    static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
-    // full and empty of each ring, then per tile s_full, p_full, pv_done, q_full; drain
-    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 8 + 1;
+    static constexpr int XCH_OFF = QS_OFF + kChunkRows * 4;     // [2 tiles][2 halves][128 rows]: exchanged between halves
+    static constexpr int BAR_OFF = XCH_OFF + 2 * kChunkRows * 4;
+    // full and empty of each ring, then per tile s_full, p_full, pv_done, q_full, turn; drain
+    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 10 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
     static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
     static constexpr int64_t PIECE = static_cast<int64_t>(kChunkRows) * (D + 2);   // floats, as FewConfig's
     static_assert(SMEM_BYTES + 256 <= 232448, "shared memory per block");
 };
-
-__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChunkRegsLow)); }
-__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChunkRegsHigh)); }
 
 // K-major int8 operand of D bytes a row: 128-byte rows in the 128-byte swizzle, or 64-byte rows
 // in the 64-byte swizzle (layout type 4), 8-row groups 8 D bytes apart.
@@ -151,6 +146,43 @@ __device__ __forceinline__ void quant_rows8(float (&v)[D / 8], int32_t g, float 
     s = zero ? 0.0f : __fmul_rn(s_z, c_g);
 }
 
+// Waits for a phase in a handful of instructions (the loops of this kernel's roles share one
+// instruction cache, and mbar_wait_bounded's clock costs six times the code). Gives up after
+// `kWaitTries` tries (each up to about a microsecond where the hardware suspends the thread):
+// then it raises `abort` and the device error word and returns false.
+constexpr uint32_t kWaitTries = 1u << 21;
+__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra AGAIN;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "n"(kWaitTries)
+        : "memory");
+    if (done == 0u) {
+        *abort = 1;
+        atomicOr(&g_device_error, kDevTimeout);
+    }
+    return done != 0u;
+}
+
+// True in one lane of the warp (all lanes call it).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
+
 // Bits [from, to) of the 32 that begin at bit `at`.
 __device__ __forceinline__ uint32_t bit_range(int32_t from, int32_t to, int32_t at)
 {
@@ -183,7 +215,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto p_full = [&](uint32_t t) { return bar0 + 8u * (TB + 2 + t); };
     auto pv_done = [&](uint32_t t) { return bar0 + 8u * (TB + 4 + t); };
     auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 6 + t); };
-    const uint32_t drain_bar = bar0 + 8u * (TB + 8);
+    auto turn = [&](uint32_t t) { return bar0 + 8u * (TB + 8 + t); };   // tile t may run its exponentials
+    const uint32_t drain_bar = bar0 + 8u * (TB + 10);
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -198,10 +231,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int s = 0; s < NB; ++s)
             mbar_init(b_full(s), 2), mbar_init(b_empty(s), 1);
         for (int s = 0; s < NS; ++s)
-            mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 8);
+            mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 16);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1), mbar_init(q_full(t), 4);
-            mbar_init(p_full(t), 4), mbar_init(pv_done(t), 1);
+            mbar_init(s_full(t), 1), mbar_init(q_full(t), 8);
+            mbar_init(p_full(t), 8), mbar_init(pv_done(t), 1), mbar_init(turn(t), 8);
         }
         mbar_init(drain_bar, 1);
         *abort = 0;
@@ -231,13 +264,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
     const int64_t count = min(first + per, total) - first;
     const int32_t pp_shift = min(p.page_shift, 6), pp = 1 << pp_shift;   // keys of a box
-    const int32_t nbox = kChunkTile >> pp_shift;
+    const int32_t nbox = kChunkTile >> pp_shift, nbox_shift = 7 - pp_shift;
     const uint32_t all_boxes = (1u << nbox) - 1u;
     auto piece_tiles = [&](int64_t n) { return static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n)); };
     auto piece_rows = [&] { return min(kChunkRows, w.s.n * p.share - w.q * kChunkRows); };
 
     if (warp < 4) {
-        regs_less();
         if (warp == 0) {
             // -------------------------------------------------------- loads
             uint32_t ks = 0, kph = 1, vs = 0, vph = 1;   // scales go with the keys (NS == NK)
@@ -251,10 +283,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // e % nbox of the piece's tile e / nbox.
                 auto fetch = [&](int32_t e0) {
                     const int32_t e = e0 + static_cast<int32_t>(lane);
-                    const int32_t i = w.i + e / nbox;
+                    const int32_t i = w.i + (e >> nbox_shift);
                     if (i >= w.i + tiles)
                         return -1;
-                    const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + (e % nbox) * pp;
+                    const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + ((e & (nbox - 1)) << pp_shift);
                     if (j >= w.s.len)
                         return -1;
                     const int32_t id = row[j >> p.page_shift];
@@ -285,8 +317,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     bool got = true;
                     if (lane == 0) {
-                        got = mbar_wait_bounded(k_empty(ks), kph, abort, p.timeout_ns) &&
-                              mbar_wait_bounded(sc_empty(ks), kph, abort, p.timeout_ns);
+                        got = mbar_wait_tries(k_empty(ks), kph, abort) &&
+                              mbar_wait_tries(sc_empty(ks), kph, abort);
                         if (got) {
                             meta[ks] = valid;
                             mbar_arrive_expect_tx(sc_full(ks), static_cast<uint32_t>(__popc(valid)) * 8u * pp);
@@ -306,7 +338,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     for (uint32_t half = 0; half < 2; ++half) {
                         const uint32_t boxes = half == 0 ? valid & ((1u << (nbox / 2)) - 1u) : valid >> (nbox / 2);
                         if (lane == 0) {
-                            got = mbar_wait_bounded(v_empty(vs), vph, abort, p.timeout_ns);
+                            got = mbar_wait_tries(v_empty(vs), vph, abort);
                             if (got)
                                 mbar_arrive_expect_tx(v_full(vs), static_cast<uint32_t>(__popc(boxes)) * pp * D);
                         }
@@ -330,18 +362,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (lane == 0) {
                 volatile int no_abort = 0;
                 for (int64_t j = nk - NK < 0 ? 0 : nk - NK; j < nk; ++j) {
-                    mbar_wait_bounded(k_full(static_cast<uint32_t>(j % NK)), static_cast<uint32_t>(j / NK) & 1u, &no_abort, p.timeout_ns);
-                    mbar_wait_bounded(sc_full(static_cast<uint32_t>(j % NS)), static_cast<uint32_t>(j / NS) & 1u, &no_abort, p.timeout_ns);
+                    mbar_wait_tries(k_full(static_cast<uint32_t>(j % NK)), static_cast<uint32_t>(j / NK) & 1u, &no_abort);
+                    mbar_wait_tries(sc_full(static_cast<uint32_t>(j % NS)), static_cast<uint32_t>(j / NS) & 1u, &no_abort);
                 }
                 for (int64_t j = nv - NV < 0 ? 0 : nv - NV; j < nv; ++j)
-                    mbar_wait_bounded(v_full(static_cast<uint32_t>(j % NV)), static_cast<uint32_t>(j / NV) & 1u, &no_abort, p.timeout_ns);
+                    mbar_wait_tries(v_full(static_cast<uint32_t>(j % NV)), static_cast<uint32_t>(j / NV) & 1u, &no_abort);
             }
         } else if (warp == 1) {
             // -------------------------------------------------------- MMA issue
             // the whole warp walks the loops, so that descriptors stay in uniform registers; one
             // lane issues
             {
-                const bool leader = lane == 0;
+                const bool leader = elect_one();
                 constexpr uint32_t IDESC_S = idesc_s8_s32(128, 128);
                 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
                 uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
@@ -349,7 +381,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 int64_t n = 0;
                 bool ok = true;
                 auto wait = [&](uint32_t bar, uint32_t parity) {
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, p.timeout_ns));
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
                     return ok;
                 };
                 // operand descriptors; 16 bytes further on is 1 more
@@ -428,27 +460,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (leader) {
                     tc_commit(drain_bar);
                     volatile int no_abort = 0;
-                    mbar_wait_bounded(drain_bar, 0u, &no_abort, p.timeout_ns);
+                    mbar_wait_tries(drain_bar, 0u, &no_abort);
                 }
             }
         } else {
             // -------------------------------------------------------- value codes to bf16
-            const uint32_t me = (warp - 2u) * 32u + lane;
+            // Eight lanes take four 16-byte chunks of the keys k and k ^ 5: the swizzles put both
+            // their loads and their stores on different banks.
             uint32_t vs = 0, vph = 0, bs = 0, bph = 1;
             bool ok = true;
             for (int64_t h = 0; ok && h < 2 * count; ++h) {
-                const bool got = mbar_wait_bounded(v_full(vs), vph, abort, p.timeout_ns) &&
-                                 mbar_wait_bounded(b_empty(bs), bph, abort, p.timeout_ns);
+                const bool got = mbar_wait_tries(v_full(vs), vph, abort) &&
+                                 mbar_wait_tries(b_empty(bs), bph, abort);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok)
                     break;
                 const uint32_t src = base + C::V_OFF + vs * C::V_STAGE, dst = base + C::B_OFF + bs * C::B_STAGE;
 #pragma unroll 2
-                for (int i = 0; i < 4 * D / 64; ++i) {
-                    const uint32_t idx = i * 64u + me, key = idx / (D / 16), c = idx % (D / 16);   // 16 dims of a key
-                    const uint32_t at = D == 128 ? key * 128u + ((c ^ (key & 7u)) << 4)
-                                                 : key * 64u + ((c ^ ((key >> 1) & 3u)) << 4);
-                    const uint4 q = lds_u4(src + at);
+                for (uint32_t i = 0; i < D / 16; ++i) {
+                    const uint32_t m = (D == 128 ? i >> 1 : i) * 8u + (warp - 2u) * 4u + (lane >> 3);
+                    const uint32_t key = (2u * m) ^ ((lane & 4u) ? 5u : 0u), atom = D == 128 ? i & 1u : 0u;
+                    const uint32_t c = (lane & 3u) + 4u * atom;   // 16 dims of a key
+                    const uint4 q = lds_u4(src + (D == 128 ? key * 128u + ((c ^ (key & 7u)) << 4)
+                                                           : key * 64u + ((c ^ ((key >> 1) & 3u)) << 4)));
                     const uint32_t x[4] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u, q.z ^ 0x80808080u, q.w ^ 0x80808080u};
                     uint32_t y[8];
 #pragma unroll
@@ -456,12 +490,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         asm("fma.rn.bf16x2 %0, %1, %2, %3;"
                             : "=r"(y[u])
                             : "r"(__byte_perm(x[u >> 1], 0u, (u & 1) ? 0x4342u : 0x4140u)), "r"(0x7f007f00u), "r"(0xc000c000u));
-                    // 128-byte rows of 64 dims; the lanes of the second 64 dims store their
-                    // chunks the other way round (their rows lie on the same banks)
-                    const uint32_t row = dst + (c >> 2) * 8192u + key * 128u, ch = 2u * (c & 3u), swap = c >> 2;
-                    const uint32_t a0 = row + (((ch + swap) ^ (key & 7u)) << 4), a1 = row + (((ch + 1u - swap) ^ (key & 7u)) << 4);
-                    sts_v4(a0, swap ? y[4] : y[0], swap ? y[5] : y[1], swap ? y[6] : y[2], swap ? y[7] : y[3]);
-                    sts_v4(a1, swap ? y[0] : y[4], swap ? y[1] : y[5], swap ? y[2] : y[6], swap ? y[3] : y[7]);
+                    const uint32_t at = dst + atom * 8192u + key * 128u + (((2u * (lane & 3u)) ^ (key & 7u)) << 4);
+                    sts_v4(at, y[0], y[1], y[2], y[3]);
+                    sts_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -476,33 +507,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
         }
     } else {
-        // ------------------------------------------------------------ softmax (warps 4..11)
-        regs_more();
-        const uint32_t tile = (warp - 4u) >> 2, quad = warp & 3u;
+        // ------------------------------------------------------------ softmax (warps 4..19)
+        // A row of logits is two threads', 64 columns each (`half`), in warps of the same TMEM
+        // lanes. After a wait gave up the loops run on to their end, without waiting and without
+        // storing results: the two warps meet at named barriers.
+        const uint32_t tile = (warp - 4u) >> 3, half = ((warp - 4u) >> 2) & 1u, quad = warp & 3u;
+        const uint32_t pair_bar = 1u + tile * 4u + quad;
         const int32_t r = static_cast<int32_t>(quad * 32u + lane);        // row in the tile
         const int32_t lr = static_cast<int32_t>(tile) * 128 + r;          // row of the segment's tile
-        const uint32_t t_lane = tmem_base + ((quad * 32u) << 16);
-        const uint32_t s_col = tile * 128u, o_col = 256u + tile * 128u;
-        uint32_t ss = 0, sph = 0, mine = 0;   // scale ring; key tiles worked on
+        const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u + half * 64u;
+        const uint32_t o_addr = tmem_base + ((quad * 32u) << 16) + 256u + tile * 128u;
+        const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + half * 16384u + static_cast<uint32_t>(r) * 128u;
+        float *xch = reinterpret_cast<float *>(smem + C::XCH_OFF) + tile * 256u;
+        uint32_t ss = 0, sph = 0, blocks = 0, mine = 0;   // scale ring; key tiles seen, and worked on
         bool ok = true, open = false;
         int64_t n = 0;
-        while (ok && n < count) {
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
+        };
+        auto swap = [&](float v) {   // the other half's value of this row
+            xch[half * 128u + r] = v;
+            bar_sync_or(pair_bar, 64, false);
+            return xch[(half ^ 1u) * 128u + r];
+        };
+        while (n < count) {
             const int32_t tiles = piece_tiles(n), rows = piece_rows(), r0 = w.q * kChunkRows;
-            const bool active = static_cast<int32_t>(tile) * 128 < rows;
-            const int32_t tok = (r0 + min(lr, rows - 1)) / p.share;
-            const int32_t pos0 = w.s.len - w.s.n;
-            const int32_t pos = pos0 + tok, low = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-            // the tile's first and last row: which key tiles are wholly visible
-            const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
-            const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
-            const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
-            if (!active) {   // no row in this tile: it only hands the scales on
-                for (int32_t k = 0; k < tiles; ++k) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sc_full(ss), sph, abort, p.timeout_ns));
-                    if (!ok)
-                        break;
-                    if (lane == 0)
+            if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile: it only hands the scales on
+                for (int32_t k = 0; k < tiles; ++k, ++blocks) {
+                    wait(sc_full(ss), sph);
+                    wait(turn(tile), (blocks & 1u) ^ (tile ^ 1u));
+                    if (lane == 0) {
+                        mbar_arrive(turn(tile ^ 1u));
                         mbar_arrive(sc_empty(ss));
+                    }
                     if (++ss == NS)
                         ss = 0, sph ^= 1u;
                 }
@@ -510,23 +547,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
             }
-            // this warp's 32 query rows, four at a time: rotated, quantized, into the operand
+            const int32_t tok = (r0 + min(lr, rows - 1)) / p.share;
+            const int32_t pos0 = w.s.len - w.s.n;
+            const int32_t pos = pos0 + tok, low = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+            // the tile's first and last row: which key tiles are wholly visible
+            const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
+            const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
+            const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
+            // this warp's 16 query rows, four at a time: rotated, quantized, into the operand
             // tile; the next four's elements are on their way meanwhile
             {
                 constexpr int E = D / 8, V = D / 64;   // elements and 16-byte vectors of a lane
+                const int32_t row0 = static_cast<int32_t>(quad * 32u + half * 16u + (lane >> 3));
                 auto load = [&](int32_t it, uint4 (&x)[V]) {
-                    const int32_t row = static_cast<int32_t>(tile) * 128 + static_cast<int32_t>(quad) * 32 + it * 4 + static_cast<int32_t>(lane >> 3);
+                    const int32_t row = static_cast<int32_t>(tile) * 128 + row0 + it * 4;
                     const int32_t tk = (r0 + row) / p.share;
                     const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + tk) * p.ldq +
                                         static_cast<int64_t>(w.kvh * p.share + r0 + row - tk * p.share) * D + (lane & 7u) * E;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        x[i] = it < 8 && row < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                        x[i] = it < 4 && row < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
                 };
                 uint4 x[V], x_next[V];
                 load(0, x);
 #pragma unroll 1
-                for (int32_t it = 0; it < 8; ++it) {
+                for (int32_t it = 0; it < 4; ++it) {
                     load(it + 1, x_next);
                     float v[E];
 #pragma unroll
@@ -542,7 +587,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     uint32_t codes[D / 32];
                     float sq;
                     quant_rows8<D>(v, p.group, p.c_g, lane, codes, sq);
-                    const uint32_t row = quad * 32u + it * 4u + (lane >> 3), c = lane & 7u;
+                    const uint32_t row = static_cast<uint32_t>(row0 + it * 4), c = lane & 7u;
                     const uint32_t at = base + C::Q_OFF + tile * C::Q_TILE + row * D;
                     if (D == 128)
                         sts_v4(at + ((c ^ (row & 7u)) << 4), codes[0], codes[1], codes[D / 32 - 2], codes[D / 32 - 1]);
@@ -556,157 +601,149 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
-            const float row_f = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
             if (lane == 0)
                 mbar_arrive(q_full(tile));
+            bar_sync_or(pair_bar, 64, false);   // the row's scale may be the other warp's
+            // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
+            const float row_f = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
             float m_used = -INFINITY, l_sum = 0.0f;
 #pragma unroll 1
-            for (int32_t k = 0; k < tiles; ++k) {
-                bool got = mbar_wait_bounded(s_full(tile), mine & 1u, abort, p.timeout_ns) &&
-                           mbar_wait_bounded(sc_full(ss), sph, abort, p.timeout_ns);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok)
-                    break;
-                tc_fence_after_sync();
+            for (int32_t k = 0; k < tiles; ++k, ++blocks) {
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
+                const uint32_t skb = base + C::SC_OFF + ss * 1024u + half * 256u;
+                wait(s_full(tile), mine & 1u);
+                wait(sc_full(ss), sph);
+                tc_fence_after_sync();
                 const uint32_t there = meta[ss];
                 const bool whole = j0 + 127 <= pos_first && (j0 >= low_last || j0 + 128 <= p.sinks) && there == all_boxes;
                 // visible columns of the 32 from c on: [low, pos] and the sinks, in pages that are there
                 auto visible = [&](int32_t c) {
+                    c += static_cast<int32_t>(half) * 64;
                     uint32_t in = 0;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
                         in |= ((there >> ((c + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
                     return in & (bit_range(low, pos + 1, j0 + c) | bit_range(0, min(p.sinks, pos + 1), j0 + c));
                 };
-                // The logits stay in TMEM, not in registers, between the two passes over them
-                // (loops of 64 columns): a row of 128 unrolled twice over overflowed the
-                // instruction cache, at 5 cycles an instruction.
-                const uint32_t skb = base + C::SC_OFF + ss * 1024u;
+                // Two passes over the row's logits, rolled loops of 32 columns with the logits kept
+                // in TMEM in between: the unrolled row had its instructions fetched anew each time.
+                uint32_t a[32];
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int32_t c = 0; c < 128; c += 64) {
-                    uint32_t a[2][32];
-                    tmem_ld_32x32b_x32(t_lane + s_col + c, a[0]);
-                    tmem_ld_32x32b_x32(t_lane + s_col + c + 32, a[1]);
+                for (int32_t c = 0; c < 64; c += 32) {
+                    tmem_ld_32x32b_x32(s_addr + c, a);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 k4 = lds_v4(skb + (c + h * 32 + e) * 4);   // a broadcast
-                            // fp32(acc) without the conversion pipe (attention.cuh), times s_k
-                            float f[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                f[u] = __uint_as_float(a[h][e + u] + 0x4B400000u);
-                            sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
-                            sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
-                            mul2(f[0], f[1], f[0], f[1], k4.x, k4.y);
-                            mul2(f[2], f[3], f[2], f[3], k4.z, k4.w);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                a[h][e + u] = __float_as_uint(f[u]);
-                        }
-                        if (!whole) {
-                            const uint32_t see = visible(c + h * 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                a[h][e] = (see >> e) & 1u ? a[h][e] : 0xff800000u;   // -inf
-                        }
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 k4 = lds_v4(skb + (c + e) * 4);   // a broadcast
+                        // fp32(acc) without the conversion pipe (attention.cuh), times s_k
+                        float f[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
+                            f[u] = __uint_as_float(a[e + u] + 0x4B400000u);
+                        sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
+                        sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
+                        mul2(f[0], f[1], f[0], f[1], k4.x, k4.y);
+                        mul2(f[2], f[3], f[2], f[3], k4.z, k4.w);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                mx[u] = max3f(mx[u], __uint_as_float(a[h][e + u]), __uint_as_float(a[h][e + u + 4]));
-                        tmem_st_32x32b_x32(t_lane + s_col + c + h * 32, a[h]);
+                        for (int u = 0; u < 4; ++u)
+                            a[e + u] = __float_as_uint(f[u]);
                     }
+                    if (!whole) {
+                        const uint32_t see = visible(c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            a[e] = (see >> e) & 1u ? a[e] : 0xff800000u;   // -inf
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            mx[u] = max3f(mx[u], __uint_as_float(a[e + u]), __uint_as_float(a[e + u + 4]));
+                    tmem_st_32x32b_x32(s_addr + c, a);
                 }
-                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
                 tmem_st_wait();
-                // the P tile is free, and O stable, once the tile's last product is done
-                if (k > 0) {
-                    got = mbar_wait_bounded(pv_done(tile), (mine & 1u) ^ 1u, abort, p.timeout_ns);
-                    ok = __all_sync(0xffffffffu, got);
-                    if (!ok)
-                        break;
-                    tc_fence_after_sync();
-                }
-                const bool grow = mb > m_used + 8.0f;
-                const bool any_grow = __any_sync(0xffffffffu, grow);
+                float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
+                // the sums are rescaled only when a row's maximum, over both halves, grows by more
+                // than 8 (weights stay below 2^8 s_v)
+                const bool any_grow = bar_sync_or(pair_bar, 64, mb > m_used + 8.0f);
                 float alpha = 1.0f;
                 if (any_grow) {
+                    mb = fmaxf(mb, swap(mb));
+                    const bool grow = mb > m_used + 8.0f;
                     alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
                 }
+                // tile 0 runs its exponentials of a key tile after tile 1 ran those of the one
+                // before, tile 1 after tile 0 ran those of the same one
+                wait(turn(tile), (blocks & 1u) ^ (tile ^ 1u));
                 // P = 2^(y - m) s_v, bf16, into the swizzled K-major tile (attention.cuh)
-                const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + static_cast<uint32_t>(r) * 128u;
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0, 0, 0, 0};
 #pragma unroll 1
-                for (int32_t c = 0; c < 128; c += 64) {
-                    uint32_t a[2][32];
-                    tmem_ld_32x32b_x32(t_lane + s_col + c, a[0]);
-                    tmem_ld_32x32b_x32(t_lane + s_col + c + 32, a[1]);
+                for (int32_t c = 0; c < 64; c += 32) {
+                    tmem_ld_32x32b_x32(s_addr + c, a);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 v4 = lds_v4(skb + 512u + (c + e) * 4);
+                        float f[4];
+                        fma2(f[0], f[1], __uint_as_float(a[e]), __uint_as_float(a[e + 1]), row_f, row_f, neg_m, neg_m);
+                        fma2(f[2], f[3], __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]), row_f, row_f, neg_m, neg_m);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 v4 = lds_v4(skb + 512u + (c + h * 32 + e) * 4);
-                            float f[4];
-                            fma2(f[0], f[1], __uint_as_float(a[h][e]), __uint_as_float(a[h][e + 1]), row_f, row_f, neg_m, neg_m);
-                            fma2(f[2], f[3], __uint_as_float(a[h][e + 2]), __uint_as_float(a[h][e + 3]), row_f, row_f, neg_m, neg_m);
+                        for (int u = 0; u < 4; ++u)
+                            f[u] = ex2_approx(f[u]);
+                        add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
+                        add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
+                        mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
+                        mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                f[u] = ex2_approx(f[u]);
-                            add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
-                            add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
-                            mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
-                            mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
+                        for (int u = 0; u < 4; ++u)
+                            a[e + u] = __float_as_uint(f[u]);
+                    }
+                    if (!whole) {   // a hidden key adds 0 whatever its scale holds
+                        const uint32_t see = visible(c);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                a[h][e + u] = __float_as_uint(f[u]);
+                        for (int e = 0; e < 32; ++e)
+                            a[e] = (see >> e) & 1u ? a[e] : 0u;
+                    }
+                    // the P tile is free, and O stable, once the tile's last product is done
+                    if (c == 0 && k > 0) {
+                        wait(pv_done(tile), (mine & 1u) ^ 1u);
+                        tc_fence_after_sync();
+                    }
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[8 * ch + 2 * u]),
+                                                                            __uint_as_float(a[8 * ch + 2 * u + 1]));
+                            x[u] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
-                        if (!whole) {   // a hidden key adds 0 whatever its scale holds
-                            const uint32_t see = visible(c + h * 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                a[h][e] = (see >> e) & 1u ? a[h][e] : 0u;
-                        }
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[h][8 * ch + 2 * u]),
-                                                                                __uint_as_float(a[h][8 * ch + 2 * u + 1]));
-                                x[u] = *reinterpret_cast<const uint32_t *>(&h2);
-                            }
-                            const uint32_t c16 = static_cast<uint32_t>(h * 4 + ch) ^ (static_cast<uint32_t>(r) & 7u);
-                            sts_v4(prow + static_cast<uint32_t>(c >> 6) * 16384u + (c16 << 4), x[0], x[1], x[2], x[3]);
-                        }
+                        const uint32_t c16 = static_cast<uint32_t>((c >> 3) + ch) ^ (static_cast<uint32_t>(r) & 7u);
+                        sts_v4(prow + (c16 << 4), x[0], x[1], x[2], x[3]);
                     }
                 }
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    mbar_arrive(turn(tile ^ 1u));
                     mbar_arrive(sc_empty(ss));
+                }
                 if (++ss == NS)
                     ss = 0, sph ^= 1u;
-                if (any_grow && k > 0) {
+                if (any_grow && k > 0) {   // this half's columns of O
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t a[32];
-                        tmem_ld_32x32b_x32(t_lane + o_col + c * 32, a);
+                    for (int32_t c = 0; c < D / 2; c += 32) {
+                        tmem_ld_32x32b_x32(o_addr + half * (D / 2) + c, a);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            a[i] = __float_as_uint(__uint_as_float(a[i]) * alpha);
-                        tmem_st_32x32b_x32(t_lane + o_col + c * 32, a);
+                        for (int e = 0; e < 32; ++e)
+                            a[e] = __float_as_uint(__uint_as_float(a[e]) * alpha);
+                        tmem_st_32x32b_x32(o_addr + half * (D / 2) + c, a);
                     }
                     tmem_st_wait();
                 }
@@ -718,49 +755,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ++mine;
             }
             const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
-            if (ok) {
-                const bool got = mbar_wait_bounded(pv_done(tile), (mine & 1u) ^ 1u, abort, p.timeout_ns);
-                ok = __all_sync(0xffffffffu, got);
-                if (ok) {
-                    tc_fence_after_sync();
-                    float v[D];
+            wait(pv_done(tile), (mine & 1u) ^ 1u);
+            tc_fence_after_sync();
+            l_sum += swap(l_sum);
+            // this half's columns of O. A whole segment's are un-rotated first: the last stage of a
+            // group of D joins the two halves, so that each thread has its own columns after it
+            const bool finish = begins && ends, join = finish && p.group == D;
+            float v[D / 2];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t a[32];
-                        tmem_ld_32x32b_x32(t_lane + o_col + c * 32, a);
-                        tmem_ld_wait();
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t x[32], y[32];
+                tmem_ld_32x32b_x32(o_addr + half * (D / 2) + c * 32, x);
+                tmem_ld_32x32b_x32(o_addr + (half ^ 1u) * (D / 2) + c * 32, y);
+                tmem_ld_wait();
+                const float own = half ? -1.0f : 1.0f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[c * 32 + i] = __uint_as_float(a[i]);
-                    }
-                    tc_fence_before_sync();
-                    if (begins && ends) {
-                        thread_butterfly<D>(v, p.group);
-                        const float inv = l_sum == 0.0f ? 0.0f : __fdiv_rn(kCodeUnit * p.c_g, l_sum);
-                        const int32_t head = w.kvh * p.share + r0 + lr - tok * p.share;   // (of a row in use)
-                        uint16_t *o = p.o + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(head) * D;
-                        if (lr < rows) {
+                for (int e = 0; e < 32; ++e)
+                    v[c * 32 + e] = join ? __fmaf_rn(__uint_as_float(x[e]), own, __uint_as_float(y[e])) : __uint_as_float(x[e]);
+            }
+            tc_fence_before_sync();
+            if (finish) {
+                thread_butterfly<D / 2>(v, p.group);
+                const float inv = l_sum == 0.0f ? 0.0f : __fdiv_rn(kCodeUnit * p.c_g, l_sum);
+                const int32_t head = w.kvh * p.share + r0 + lr - tok * p.share;   // (of a row in use)
+                uint16_t *o = p.o + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(head) * D + half * (D / 2);
+                if (ok && lr < rows) {
 #pragma unroll
-                            for (int i = 0; i < D / 8; ++i) {
-                                uint32_t x[4];
+                    for (int e = 0; e < D / 16; ++e) {
+                        uint32_t x[4];
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * i + 2 * u] * inv, v[8 * i + 2 * u + 1] * inv);
-                                    x[u] = *reinterpret_cast<const uint32_t *>(&h2);
-                                }
-                                st_v4(o + 8 * i, x[0], x[1], x[2], x[3]);
-                            }
+                        for (int u = 0; u < 4; ++u) {
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * e + 2 * u] * inv, v[8 * e + 2 * u + 1] * inv);
+                            x[u] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
-                    } else if (lr < rows) {
-                        float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
-#pragma unroll
-                        for (int i = 0; i < D / 4; ++i)
-                            *reinterpret_cast<float4 *>(ws + lr * D + 4 * i) =
-                                make_float4(v[4 * i] * kCodeUnit, v[4 * i + 1] * kCodeUnit, v[4 * i + 2] * kCodeUnit,
-                                            v[4 * i + 3] * kCodeUnit);
-                        *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, l_sum);
+                        st_v4(o + 8 * e, x[0], x[1], x[2], x[3]);
                     }
                 }
+            } else if (lr < rows) {
+                float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e)
+                    *reinterpret_cast<float4 *>(ws + lr * D + half * (D / 2) + 4 * e) =
+                        make_float4(v[4 * e] * kCodeUnit, v[4 * e + 1] * kCodeUnit, v[4 * e + 2] * kCodeUnit,
+                                    v[4 * e + 3] * kCodeUnit);
+                if (half == 0u)
+                    *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, l_sum);
             }
             n += tiles;
             if (threadIdx.x == 128 && begins && !ends) {

@@ -172,14 +172,8 @@ sdnq_status launch_chunk(const PagedParams &p, const DeviceInfo &dev, int sms, c
     const uint32_t page = 1u << p.page_shift;
     if (!make_pool_map<D>(&map, p, page <= kChunkBox ? page : kChunkBox))
         return SDNQ_ERR_CUDA;
-    static PerDeviceCache<1> smem, regs;
-    // the kernel's warpgroups hand registers over: it must have been compiled with the number
-    // that the split assumes, or its wait for them would not end
-    const bool fits = regs.get(dev.index, 0, [&] {
-        cudaFuncAttributes a = {};
-        return cudaFuncGetAttributes(&a, attn_chunk_kernel<D>) == cudaSuccess && a.numRegs == kChunkRegs ? 1 : -1;
-    }) == 1;
-    if (!fits || !smem_attr_once(smem, dev.index, attn_chunk_kernel<D>, C::SMEM_BYTES)) {
+    static PerDeviceCache<1> smem;
+    if (!smem_attr_once(smem, dev.index, attn_chunk_kernel<D>, C::SMEM_BYTES)) {
         cudaGetLastError();
         return SDNQ_ERR_CUDA;
     }
