@@ -2,49 +2,45 @@
 // 5th-generation tensor cores. The mathematics and the work split are attention_paged.cuh's.
 //
 // One persistent block per SM, 256 query rows of one kv head at a time (two tiles of 128 that
-// share every key and value), keys in tiles of 128:
+// share every key and value), keys in steps of 64:
 // - warp 0 streams keys, values and scales page by page through TMA rings;
-// - warps 2 and 3 turn each half tile of value codes into bf16 (times 2^-6, exact), the
+// - warps 2 and 3 turn each step's value codes into bf16 (times 2^-6, exact), the
 //   128-byte-swizzled operand of the second product;
-// - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) and O_t += P_t V
-//   (kind::f16, fp32 in TMEM) for both tiles;
+// - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) two steps ahead of
+//   O_t += P_t V (kind::f16, fp32 in TMEM): logits and P of a tile have two buffers each, so
+//   that its softmax never waits for a product just issued (128-key steps with one buffer
+//   spent 3500 cycles a step in hand-overs alone);
 // - warps 4..7 (tile 0) and 8..11 (tile 1), one thread a query row, rotate and quantize their
-//   query rows into the operand tile, then per key tile form base-2 logits, an online softmax
-//   (sums rescaled only when the maximum grows by more than 2^8), and P = probability * s_v in
-//   bf16. At the end of a segment the thread has its
-//   output row in registers: the rotation is undone there.
-// Bound: the exponentials. Per 256 x 128 tile the SM's 16 exponentials a cycle take 2048
-// cycles, the instructions of softmax and conversion about 1900 issue cycles a scheduler, the
-// two products 256 + 512 tensor cycles, 33 KB of codes from L2 or memory about 1400.
-// The two softmax warpgroups take registers over from the first one (setmaxnreg), so that a
-// thread holds a whole row of logits.
+//   query rows into the operand tile, then per step form 64 base-2 logits, an online softmax
+//   (sums rescaled only when the maximum grows by more than 8), and P = probability * s_v in
+//   bf16. At the end of a segment the rotation is undone in registers.
+// Code size matters: the roles share one instruction cache, and a loop body that overflows it
+// runs several times slower; so the loops are small, rolled where they can be.
 #pragma once
 
 #include "attention_paged.cuh"
 
 namespace sdnq {
 
-constexpr int kChunkTile = 128;     // keys per step
+constexpr int kChunkTile = 64;      // keys per step
 constexpr int kChunkRows = 256;     // query rows of a segment: two tiles of 128
-constexpr int kChunkBox = 64;       // keys of a box at most
-constexpr int kChunkThreads = 640;
+constexpr int kChunkThreads = 384;
 
 template <int D>
 struct ChunkConfig {
-    static constexpr int NK = 3, NV = 3, NB = 3, NS = 3;   // stages: K, value codes, bf16 values (halves), scales
-    static constexpr int Q_TILE = 128 * D, K_STAGE = 128 * D, V_STAGE = 64 * D, B_STAGE = 64 * D * 2;
-    static constexpr int P_TILE = 128 * 128 * 2;
+    static constexpr int NK = 4, NV = 3, NB = 4, NS = 6;   // stages: K, value codes, bf16 values, scales
+    static constexpr int Q_TILE = 128 * D, K_STAGE = 64 * D, V_STAGE = 64 * D, B_STAGE = 64 * D * 2;
+    static constexpr int P_BUF = 128 * 64 * 2;
     static constexpr int Q_OFF = 0;
-    static constexpr int P_OFF = Q_OFF + 2 * Q_TILE;
-    static constexpr int K_OFF = P_OFF + 2 * P_TILE;
+    static constexpr int P_OFF = Q_OFF + 2 * Q_TILE;        // [2 tiles][2 buffers]
+    static constexpr int K_OFF = P_OFF + 4 * P_BUF;
     static constexpr int B_OFF = K_OFF + NK * K_STAGE;
     static constexpr int V_OFF = B_OFF + NB * B_STAGE;
-    static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 128 key scales, 128 value scales a stage
-    static constexpr int QS_OFF = SC_OFF + NS * 1024;       // query scales
-    static constexpr int XCH_OFF = QS_OFF + kChunkRows * 4;     // [2 tiles][2 halves][128 rows]: exchanged between halves
-    static constexpr int BAR_OFF = XCH_OFF + 2 * kChunkRows * 4;
-    // full and empty of each ring, then per tile s_full, p_full, pv_done, q_full, turn; drain
-    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 10 + 1;
+    static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 64 key scales, 64 value scales a stage
+    static constexpr int QS_OFF = SC_OFF + NS * 512;        // query scales
+    static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
+    // full and empty of each ring, then per tile and buffer s_full, p_full, pv_done; q_full; drain
+    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 12 + 2 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
     static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
@@ -210,13 +206,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto b_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV) + NB + s); };
     auto sc_full = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + s); };
     auto sc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + NS + s); };
+    // per tile t and buffer b, one phase every other step: S written, P written, P V done
     constexpr int TB = 2 * (NK + NV + NB + NS);
-    auto s_full = [&](uint32_t t) { return bar0 + 8u * (TB + t); };
-    auto p_full = [&](uint32_t t) { return bar0 + 8u * (TB + 2 + t); };
-    auto pv_done = [&](uint32_t t) { return bar0 + 8u * (TB + 4 + t); };
-    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 6 + t); };
-    auto turn = [&](uint32_t t) { return bar0 + 8u * (TB + 8 + t); };   // tile t may run its exponentials
-    const uint32_t drain_bar = bar0 + 8u * (TB + 10);
+    auto s_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 2 * t + b); };
+    auto p_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 4 + 2 * t + b); };
+    auto pv_done = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 8 + 2 * t + b); };
+    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 12 + t); };
+    const uint32_t drain_bar = bar0 + 8u * (TB + 14);
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -231,10 +227,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int s = 0; s < NB; ++s)
             mbar_init(b_full(s), 2), mbar_init(b_empty(s), 1);
         for (int s = 0; s < NS; ++s)
-            mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 16);
+            mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 8);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1), mbar_init(q_full(t), 8);
-            mbar_init(p_full(t), 8), mbar_init(pv_done(t), 1), mbar_init(turn(t), 8);
+            for (int b = 0; b < 2; ++b)
+                mbar_init(s_full(t, b), 1), mbar_init(p_full(t, b), 4), mbar_init(pv_done(t, b), 1);
+            mbar_init(q_full(t), 4);
         }
         mbar_init(drain_bar, 1);
         *abort = 0;
@@ -264,301 +261,245 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
     const int64_t count = min(first + per, total) - first;
     const int32_t pp_shift = min(p.page_shift, 6), pp = 1 << pp_shift;   // keys of a box
-    const int32_t nbox = kChunkTile >> pp_shift, nbox_shift = 7 - pp_shift;
+    const int32_t nbox_shift = 6 - pp_shift, nbox = 1 << nbox_shift;
     const uint32_t all_boxes = (1u << nbox) - 1u;
-    auto piece_tiles = [&](int64_t n) { return static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n)); };
+    auto piece_steps = [&](int64_t n) { return static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n)); };
     auto piece_rows = [&] { return min(kChunkRows, w.s.n * p.share - w.q * kChunkRows); };
+    // A role that gave up waiting runs its loops to their end without waiting or storing.
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
+        return ok;
+    };
 
-    if (warp < 4) {
-        if (warp == 0) {
-            // -------------------------------------------------------- loads
-            uint32_t ks = 0, kph = 1, vs = 0, vph = 1;   // scales go with the keys (NS == NK)
-            static_assert(NS == NK, "one slot number serves keys and scales");
-            int64_t n = 0, nv = 0, nk = 0;
-            bool ok = true;
-            while (ok && n < count) {
-                const int32_t tiles = piece_tiles(n);
-                const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
-                // Page ids are read 32 at a time, a batch ahead of their use; entry e is box
-                // e % nbox of the piece's tile e / nbox.
-                auto fetch = [&](int32_t e0) {
-                    const int32_t e = e0 + static_cast<int32_t>(lane);
-                    const int32_t i = w.i + (e >> nbox_shift);
-                    if (i >= w.i + tiles)
-                        return -1;
-                    const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + ((e & (nbox - 1)) << pp_shift);
-                    if (j >= w.s.len)
-                        return -1;
-                    const int32_t id = row[j >> p.page_shift];
-                    if (id < 0 || id >= p.pages) {
-                        atomicOr(&g_device_error, kDevIndex);
-                        return -1;
-                    }
-                    return id;
-                };
-                int32_t ids = fetch(0), ids_next = fetch(32), e0 = 0;
-                for (int32_t k = 0; ok && k < tiles; ++k) {
-                    if (k * nbox >= e0 + 32) {
-                        ids = ids_next;
-                        e0 += 32;
-                        ids_next = fetch(e0 + 32);
-                    }
-                    // lane c < nbox has box c of this tile
-                    const int32_t id = __shfl_sync(0xffffffffu, ids, (k * nbox - e0 + static_cast<int32_t>(lane)) & 31);
-                    const bool mine = static_cast<int32_t>(lane) < nbox && id >= 0;
-                    const uint32_t valid = __ballot_sync(0xffffffffu, mine);
-                    const int32_t i = w.i + k;
-                    const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + static_cast<int32_t>(lane) * pp;
-                    int32_t krow = 0, vrow = 0;
-                    if (mine) {
-                        krow = static_cast<int32_t>(((static_cast<int64_t>(id) * p.Hkv + w.kvh) * 2) << p.page_shift) +
-                               (j & ((1 << p.page_shift) - 1));
-                        vrow = krow + (1 << p.page_shift);
-                    }
-                    bool got = true;
-                    if (lane == 0) {
-                        got = mbar_wait_tries(k_empty(ks), kph, abort) &&
-                              mbar_wait_tries(sc_empty(ks), kph, abort);
-                        if (got) {
-                            meta[ks] = valid;
-                            mbar_arrive_expect_tx(sc_full(ks), static_cast<uint32_t>(__popc(valid)) * 8u * pp);
-                            mbar_arrive_expect_tx(k_full(ks), static_cast<uint32_t>(__popc(valid)) * pp * D);
-                        }
-                    }
-                    ok = __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
-                    if (!ok)
-                        break;
-                    ++nk;
-                    if (mine) {
-                        tma_load_2d(base + C::K_OFF + ks * C::K_STAGE + lane * pp * D, &tmPool, k_full(ks), 0, krow);
-                        const uint32_t sdst = base + C::SC_OFF + ks * 1024u + lane * pp * 4u;
-                        bulk_load_1d(sdst, p.scales + krow, 4u * pp, sc_full(ks));
-                        bulk_load_1d(sdst + 512u, p.scales + vrow, 4u * pp, sc_full(ks));
-                    }
-                    for (uint32_t half = 0; half < 2; ++half) {
-                        const uint32_t boxes = half == 0 ? valid & ((1u << (nbox / 2)) - 1u) : valid >> (nbox / 2);
-                        if (lane == 0) {
-                            got = mbar_wait_tries(v_empty(vs), vph, abort);
-                            if (got)
-                                mbar_arrive_expect_tx(v_full(vs), static_cast<uint32_t>(__popc(boxes)) * pp * D);
-                        }
-                        ok = __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
-                        if (!ok)
-                            break;
-                        ++nv;
-                        const uint32_t box = lane - half * (nbox / 2);
-                        if (mine && box < static_cast<uint32_t>(nbox / 2))
-                            tma_load_2d(base + C::V_OFF + vs * C::V_STAGE + box * pp * D, &tmPool, v_full(vs), 0, vrow);
-                        if (++vs == NV)
-                            vs = 0, vph ^= 1u;
-                    }
-                    if (++ks == NK)
-                        ks = 0, kph ^= 1u;
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        uint32_t ks = 0, kph = 1, vs = 0, vph = 1, ss = 0, sph = 1;
+        int64_t n = 0, issued = 0;
+        while (ok && n < count) {
+            const int32_t steps = piece_steps(n);
+            const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
+            // Page ids are read 32 at a time, a batch ahead of their use; entry e is box
+            // e % nbox of the piece's step e / nbox.
+            auto fetch = [&](int32_t e0) {
+                const int32_t e = e0 + static_cast<int32_t>(lane);
+                const int32_t i = w.i + (e >> nbox_shift);
+                if (i >= w.i + steps)
+                    return -1;
+                const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + ((e & (nbox - 1)) << pp_shift);
+                if (j >= w.s.len)
+                    return -1;
+                const int32_t id = row[j >> p.page_shift];
+                if (id < 0 || id >= p.pages) {
+                    atomicOr(&g_device_error, kDevIndex);
+                    return -1;
                 }
-                n += tiles;
-                walk_next_segment<kChunkTile, kChunkRows>(p, w);
-            }
-            // every copy has landed before the block may end
-            if (lane == 0) {
-                volatile int no_abort = 0;
-                for (int64_t j = nk - NK < 0 ? 0 : nk - NK; j < nk; ++j) {
-                    mbar_wait_tries(k_full(static_cast<uint32_t>(j % NK)), static_cast<uint32_t>(j / NK) & 1u, &no_abort);
-                    mbar_wait_tries(sc_full(static_cast<uint32_t>(j % NS)), static_cast<uint32_t>(j / NS) & 1u, &no_abort);
-                }
-                for (int64_t j = nv - NV < 0 ? 0 : nv - NV; j < nv; ++j)
-                    mbar_wait_tries(v_full(static_cast<uint32_t>(j % NV)), static_cast<uint32_t>(j / NV) & 1u, &no_abort);
-            }
-        } else if (warp == 1) {
-            // -------------------------------------------------------- MMA issue
-            // the whole warp walks the loops, so that descriptors stay in uniform registers; one
-            // lane issues
-            {
-                const bool leader = elect_one();
-                constexpr uint32_t IDESC_S = idesc_s8_s32(128, 128);
-                constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
-                uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
-                uint32_t q_n = 0, p_n = 0;   // bit t: pieces, and products with V, of tile t so far, mod 2
-                int64_t n = 0;
-                bool ok = true;
-                auto wait = [&](uint32_t bar, uint32_t parity) {
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
-                    return ok;
-                };
-                // operand descriptors; 16 bytes further on is 1 more
-                const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
-                const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
-                // S_t = Q_t K^T of the key tile in slot ks; the last tile's frees the slot
-                auto issue_s = [&](uint32_t t, bool last) {
-                    tc_fence_after_sync();
-                    const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
-                    if (leader) {
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k)
-                            mma_s8(tmem_base + t * 128, qa + 2 * k, ka + 2 * k, IDESC_S, k != 0 ? 1u : 0u);
-                        tc_commit(s_full(t));
-                        if (last)
-                            tc_commit(k_empty(ks));
-                    }
-                    __syncwarp();
-                    if (last) {
-                        if (++ks == NK)
-                            ks = 0, kph ^= 1u;
-                    }
-                };
-                while (ok && n < count) {
-                    const int32_t tiles = piece_tiles(n);
-                    const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
-                    // key tile k's S_t is issued when P_t of the one before is written (S_t has
-                    // been read then), and before that one's product with V, so that the tile's
-                    // softmax goes on while the product runs
+                return id;
+            };
+            int32_t ids = -1, ids_next = -1;
 #pragma unroll 1
-                    for (int32_t k = 0; ok && k <= tiles; ++k) {
-                        if (k < tiles)
-                            wait(k_full(ks), kph);
-#pragma unroll 1
-                        for (uint32_t t = 0; ok && t < in_use; ++t) {
-                            if (k == 0 ? !wait(q_full(t), (q_n >> t) & 1u) : !wait(p_full(t), (p_n >> t) & 1u))
-                                break;
-                            if (k < tiles)
-                                issue_s(t, t + 1 == in_use);
-                            if (k == 0) {
-                                q_n ^= 1u << t;
-                                continue;
-                            }
-                            uint32_t slot = bs, ph = bph;
-#pragma unroll 1
-                            for (uint32_t half = 0; half < 2; ++half) {
-                                if (!wait(b_full(slot), ph))
-                                    break;
-                                tc_fence_after_sync();
-                                const uint64_t pa = dp + t * (C::P_TILE >> 4) + half * (16384u >> 4);
-                                const uint64_t va = db + slot * (C::B_STAGE >> 4);
-                                if (leader) {
-#pragma unroll
-                                    for (int kk = 0; kk < 4; ++kk)
-                                        mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV,
-                                                ((k - 1) | static_cast<int32_t>(half) | kk) != 0 ? 1u : 0u);
-                                    if (t + 1 == in_use)
-                                        tc_commit(b_empty(slot));
-                                    if (half == 1)
-                                        tc_commit(pv_done(t));
-                                }
-                                __syncwarp();
-                                if (++slot == NB)
-                                    slot = 0, ph ^= 1u;
-                            }
-                            if (!ok)
-                                break;
-                            p_n ^= 1u << t;
-                            if (t + 1 == in_use)
-                                bs = slot, bph = ph;
-                        }
-                    }
-                    n += tiles;
-                    walk_next_segment<kChunkTile, kChunkRows>(p, w);
+            for (int32_t k = 0; k < steps; ++k) {
+                const int32_t at = (k << nbox_shift) & 31;
+                if (at == 0) {
+                    ids = k == 0 ? fetch(0) : ids_next;
+                    ids_next = fetch((k << nbox_shift) + 32);
                 }
-                if (leader) {
-                    tc_commit(drain_bar);
-                    volatile int no_abort = 0;
-                    mbar_wait_tries(drain_bar, 0u, &no_abort);
-                }
-            }
-        } else {
-            // -------------------------------------------------------- value codes to bf16
-            // Eight lanes take four 16-byte chunks of the keys k and k ^ 5: the swizzles put both
-            // their loads and their stores on different banks.
-            uint32_t vs = 0, vph = 0, bs = 0, bph = 1;
-            bool ok = true;
-            for (int64_t h = 0; ok && h < 2 * count; ++h) {
-                const bool got = mbar_wait_tries(v_full(vs), vph, abort) &&
-                                 mbar_wait_tries(b_empty(bs), bph, abort);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok)
+                // lane c < nbox has box c of this step
+                const int32_t id = __shfl_sync(0xffffffffu, ids, (at + static_cast<int32_t>(lane)) & 31);
+                const bool mine = static_cast<int32_t>(lane) < nbox && id >= 0;
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine);
+                const uint32_t keys = static_cast<uint32_t>(__popc(valid)) << pp_shift;
+                const int32_t i = w.i + k;
+                const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + (static_cast<int32_t>(lane) << pp_shift);
+                const int32_t krow = mine ? static_cast<int32_t>(((static_cast<int64_t>(id) * p.Hkv + w.kvh) * 2) << p.page_shift) +
+                                                (j & ((1 << p.page_shift) - 1))
+                                          : 0;
+                const int32_t vrow = krow + (1 << p.page_shift);
+                if (!wait(k_empty(ks), kph) || !wait(sc_empty(ss), sph) || !wait(v_empty(vs), vph))
                     break;
-                const uint32_t src = base + C::V_OFF + vs * C::V_STAGE, dst = base + C::B_OFF + bs * C::B_STAGE;
-#pragma unroll 2
-                for (uint32_t i = 0; i < D / 16; ++i) {
-                    const uint32_t m = (D == 128 ? i >> 1 : i) * 8u + (warp - 2u) * 4u + (lane >> 3);
-                    const uint32_t key = (2u * m) ^ ((lane & 4u) ? 5u : 0u), atom = D == 128 ? i & 1u : 0u;
-                    const uint32_t c = (lane & 3u) + 4u * atom;   // 16 dims of a key
-                    const uint4 q = lds_u4(src + (D == 128 ? key * 128u + ((c ^ (key & 7u)) << 4)
-                                                           : key * 64u + ((c ^ ((key >> 1) & 3u)) << 4)));
-                    const uint32_t x[4] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u, q.z ^ 0x80808080u, q.w ^ 0x80808080u};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)   // as codes_to_bf16x2, two dims of one key
-                        asm("fma.rn.bf16x2 %0, %1, %2, %3;"
-                            : "=r"(y[u])
-                            : "r"(__byte_perm(x[u >> 1], 0u, (u & 1) ? 0x4342u : 0x4140u)), "r"(0x7f007f00u), "r"(0xc000c000u));
-                    const uint32_t at = dst + atom * 8192u + key * 128u + (((2u * (lane & 3u)) ^ (key & 7u)) << 4);
-                    sts_v4(at, y[0], y[1], y[2], y[3]);
-                    sts_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(b_full(bs));
-                    mbar_arrive(v_empty(vs));
+                    meta[ss] = valid;
+                    mbar_arrive_expect_tx(k_full(ks), keys * D);
+                    mbar_arrive_expect_tx(sc_full(ss), keys * 8u);
+                    mbar_arrive_expect_tx(v_full(vs), keys * D);
                 }
+                __syncwarp();
+                ++issued;
+                if (mine) {
+                    tma_load_2d(base + C::K_OFF + ks * C::K_STAGE + lane * pp * D, &tmPool, k_full(ks), 0, krow);
+                    const uint32_t sdst = base + C::SC_OFF + ss * 512u + lane * pp * 4u;
+                    bulk_load_1d(sdst, p.scales + krow, 4u * pp, sc_full(ss));
+                    bulk_load_1d(sdst + 256u, p.scales + vrow, 4u * pp, sc_full(ss));
+                    tma_load_2d(base + C::V_OFF + vs * C::V_STAGE + lane * pp * D, &tmPool, v_full(vs), 0, vrow);
+                }
+                if (++ks == NK)
+                    ks = 0, kph ^= 1u;
+                if (++ss == NS)
+                    ss = 0, sph ^= 1u;
                 if (++vs == NV)
                     vs = 0, vph ^= 1u;
-                if (++bs == NB)
+            }
+            n += steps;
+            walk_next_segment<kChunkTile, kChunkRows>(p, w);
+        }
+        // every copy has landed before the block may end
+        ok = true;
+        auto drain = [&](uint32_t bar, int stages) {
+            for (int64_t j = issued - stages < 0 ? 0 : issued - stages; j < issued; ++j)
+                mbar_wait_tries(bar + 8u * static_cast<uint32_t>(j % stages), static_cast<uint32_t>(j / stages) & 1u, abort);
+        };
+        drain(k_full(0), NK);
+        drain(sc_full(0), NS);
+        drain(v_full(0), NV);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issue
+        // The whole warp walks the loops, so that descriptors stay in uniform registers; one lane
+        // issues.
+        const bool leader = elect_one();
+        constexpr uint32_t IDESC_S = idesc_s8_s32(128, 64);
+        constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
+        // operand descriptors; 16 bytes further on is 1 more
+        const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
+        const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
+        uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
+        uint32_t g0 = 0, g1 = 0, q_n = 0;   // steps of tiles 0 and 1 before this piece; bit t: tile t's pieces, mod 2
+        int64_t n = 0;
+        while (ok && n < count) {
+            const int32_t steps = piece_steps(n);
+            const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
+            // S_t of step k goes out when P_t of step k - 2 is written (that S buffer has been
+            // read then), just before the product of that P with V
+#pragma unroll 1
+            for (int32_t k = 0; ok && k < steps + 2; ++k) {
+                if (k < steps)
+                    wait(k_full(ks), kph);
+                if (k >= 2)
+                    wait(b_full(bs), bph);
+#pragma unroll 1
+                for (uint32_t t = 0; t < in_use; ++t) {
+                    const uint32_t g = (t == 0 ? g0 : g1) + static_cast<uint32_t>(k), b = g & 1u;   // step k, and k - 2's buffers
+                    if (k == 0) {
+                        wait(q_full(t), (q_n >> t) & 1u);
+                        q_n ^= 1u << t;
+                    }
+                    if (k >= 2)
+                        wait(p_full(t, b), ((g >> 1) & 1u) ^ 1u);
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
+                    const uint64_t pa = dp + (2 * t + b) * (C::P_BUF >> 4), va = db + bs * (C::B_STAGE >> 4);
+                    if (leader) {
+                        if (k < steps) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                mma_s8(tmem_base + t * 128 + b * 64, qa + 2 * kk, ka + 2 * kk, IDESC_S, kk != 0 ? 1u : 0u);
+                            tc_commit(s_full(t, b));
+                            if (t + 1 == in_use)
+                                tc_commit(k_empty(ks));
+                        }
+                        if (k >= 2) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, k > 2 || kk != 0 ? 1u : 0u);
+                            tc_commit(pv_done(t, b));
+                            if (t + 1 == in_use)
+                                tc_commit(b_empty(bs));
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (k < steps && ++ks == NK)
+                    ks = 0, kph ^= 1u;
+                if (k >= 2 && ++bs == NB)
                     bs = 0, bph ^= 1u;
             }
+            g0 += static_cast<uint32_t>(steps);
+            g1 += in_use == 2 ? static_cast<uint32_t>(steps) : 0u;
+            n += steps;
+            walk_next_segment<kChunkTile, kChunkRows>(p, w);
+        }
+        if (leader) {
+            tc_commit(drain_bar);
+            mbar_wait_tries(drain_bar, 0u, abort);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ value codes to bf16
+        // Eight lanes take four 16-byte chunks of the keys k and k ^ 5: the swizzles put both
+        // their loads and their stores on different banks.
+        uint32_t vs = 0, vph = 0, bs = 0, bph = 1;
+#pragma unroll 1
+        for (int64_t h = 0; h < count; ++h) {
+            if (!wait(v_full(vs), vph) || !wait(b_empty(bs), bph))
+                break;
+            const uint32_t src = base + C::V_OFF + vs * C::V_STAGE, dst = base + C::B_OFF + bs * C::B_STAGE;
+#pragma unroll 2
+            for (uint32_t i = 0; i < D / 16; ++i) {
+                const uint32_t m = (D == 128 ? i >> 1 : i) * 8u + (warp - 2u) * 4u + (lane >> 3);
+                const uint32_t key = (2u * m) ^ ((lane & 4u) ? 5u : 0u), atom = D == 128 ? i & 1u : 0u;
+                const uint32_t c = (lane & 3u) + 4u * atom;   // 16 dims of a key
+                const uint4 q = lds_u4(src + (D == 128 ? key * 128u + ((c ^ (key & 7u)) << 4)
+                                                       : key * 64u + ((c ^ ((key >> 1) & 3u)) << 4)));
+                const uint32_t x[4] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u, q.z ^ 0x80808080u, q.w ^ 0x80808080u};
+                uint32_t y[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)   // as codes_to_bf16x2, two dims of one key
+                    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+                        : "=r"(y[u])
+                        : "r"(__byte_perm(x[u >> 1], 0u, (u & 1) ? 0x4342u : 0x4140u)), "r"(0x7f007f00u), "r"(0xc000c000u));
+                const uint32_t at = dst + atom * 8192u + key * 128u + (((2u * (lane & 3u)) ^ (key & 7u)) << 4);
+                sts_v4(at, y[0], y[1], y[2], y[3]);
+                sts_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(b_full(bs));
+                mbar_arrive(v_empty(vs));
+            }
+            if (++vs == NV)
+                vs = 0, vph ^= 1u;
+            if (++bs == NB)
+                bs = 0, bph ^= 1u;
         }
     } else {
-        // ------------------------------------------------------------ softmax (warps 4..19)
-        // A row of logits is two threads', 64 columns each (`half`), in warps of the same TMEM
-        // lanes. After a wait gave up the loops run on to their end, without waiting and without
-        // storing results: the two warps meet at named barriers.
-        const uint32_t tile = (warp - 4u) >> 3, half = ((warp - 4u) >> 2) & 1u, quad = warp & 3u;
-        const uint32_t pair_bar = 1u + tile * 4u + quad;
+        // ------------------------------------------------------------ softmax (warps 4..11)
+        const uint32_t tile = (warp - 4u) >> 2, quad = warp & 3u;
         const int32_t r = static_cast<int32_t>(quad * 32u + lane);        // row in the tile
         const int32_t lr = static_cast<int32_t>(tile) * 128 + r;          // row of the segment's tile
-        const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u + half * 64u;
-        const uint32_t o_addr = tmem_base + ((quad * 32u) << 16) + 256u + tile * 128u;
-        const uint32_t prow = base + C::P_OFF + tile * C::P_TILE + half * 16384u + static_cast<uint32_t>(r) * 128u;
-        float *xch = reinterpret_cast<float *>(smem + C::XCH_OFF) + tile * 256u;
-        uint32_t ss = 0, sph = 0, blocks = 0, mine = 0;   // scale ring; key tiles seen, and worked on
-        bool ok = true, open = false;
+        const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u;
+        const uint32_t o_addr = s_addr + 256u;
+        const uint32_t prow = base + C::P_OFF + tile * 2u * C::P_BUF + static_cast<uint32_t>(r) * 128u;
+        uint32_t ss = 0, sph = 0, g = 0;   // scale ring; steps of this tile
+        bool open = false;
         int64_t n = 0;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
-        };
-        auto swap = [&](float v) {   // the other half's value of this row
-            xch[half * 128u + r] = v;
-            bar_sync_or(pair_bar, 64, false);
-            return xch[(half ^ 1u) * 128u + r];
-        };
         while (n < count) {
-            const int32_t tiles = piece_tiles(n), rows = piece_rows(), r0 = w.q * kChunkRows;
+            const int32_t steps = piece_steps(n), rows = piece_rows(), r0 = w.q * kChunkRows;
             if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile: it only hands the scales on
-                for (int32_t k = 0; k < tiles; ++k, ++blocks) {
+#pragma unroll 1
+                for (int32_t k = 0; k < steps; ++k) {
                     wait(sc_full(ss), sph);
-                    wait(turn(tile), (blocks & 1u) ^ (tile ^ 1u));
-                    if (lane == 0) {
-                        mbar_arrive(turn(tile ^ 1u));
+                    if (lane == 0)
                         mbar_arrive(sc_empty(ss));
-                    }
                     if (++ss == NS)
                         ss = 0, sph ^= 1u;
                 }
-                n += tiles;
+                n += steps;
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
             }
             const int32_t tok = (r0 + min(lr, rows - 1)) / p.share;
             const int32_t pos0 = w.s.len - w.s.n;
             const int32_t pos = pos0 + tok, low = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-            // the tile's first and last row: which key tiles are wholly visible
+            // the tile's first and last row: which steps are wholly visible
             const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
             const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
             const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
-            // this warp's 16 query rows, four at a time: rotated, quantized, into the operand
+            // this warp's 32 query rows, four at a time: rotated, quantized, into the operand
             // tile; the next four's elements are on their way meanwhile
             {
                 constexpr int E = D / 8, V = D / 64;   // elements and 16-byte vectors of a lane
-                const int32_t row0 = static_cast<int32_t>(quad * 32u + half * 16u + (lane >> 3));
+                const int32_t row0 = static_cast<int32_t>(quad * 32u + (lane >> 3));
                 auto load = [&](int32_t it, uint4 (&x)[V]) {
                     const int32_t row = static_cast<int32_t>(tile) * 128 + row0 + it * 4;
                     const int32_t tk = (r0 + row) / p.share;
@@ -566,12 +507,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                         static_cast<int64_t>(w.kvh * p.share + r0 + row - tk * p.share) * D + (lane & 7u) * E;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        x[i] = it < 4 && row < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+                        x[i] = it < 8 && row < rows ? ld_nc_v4(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
                 };
                 uint4 x[V], x_next[V];
                 load(0, x);
 #pragma unroll 1
-                for (int32_t it = 0; it < 4; ++it) {
+                for (int32_t it = 0; it < 8; ++it) {
                     load(it + 1, x_next);
                     float v[E];
 #pragma unroll
@@ -601,97 +542,106 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_full(tile));
-            bar_sync_or(pair_bar, 64, false);   // the row's scale may be the other warp's
             // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
             const float row_f = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
+            if (lane == 0)
+                mbar_arrive(q_full(tile));
             float m_used = -INFINITY, l_sum = 0.0f;
 #pragma unroll 1
-            for (int32_t k = 0; k < tiles; ++k, ++blocks) {
+            for (int32_t k = 0; k < steps; ++k, ++g) {
+                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
-                const uint32_t skb = base + C::SC_OFF + ss * 1024u + half * 256u;
-                wait(s_full(tile), mine & 1u);
+                const uint32_t skb = base + C::SC_OFF + ss * 512u;
+                wait(s_full(tile, b), ph);
                 wait(sc_full(ss), sph);
                 tc_fence_after_sync();
                 const uint32_t there = meta[ss];
-                const bool whole = j0 + 127 <= pos_first && (j0 >= low_last || j0 + 128 <= p.sinks) && there == all_boxes;
-                // visible columns of the 32 from c on: [low, pos] and the sinks, in pages that are there
-                auto visible = [&](int32_t c) {
-                    c += static_cast<int32_t>(half) * 64;
-                    uint32_t in = 0;
+                const bool whole = j0 + 63 <= pos_first && (j0 >= low_last || j0 + 64 <= p.sinks) && there == all_boxes;
+                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+                if (!whole) {   // visible columns: [low, pos] and the sinks, in pages that are there
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        in |= ((there >> ((c + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
-                    return in & (bit_range(low, pos + 1, j0 + c) | bit_range(0, min(p.sinks, pos + 1), j0 + c));
-                };
-                // Two passes over the row's logits, rolled loops of 32 columns with the logits kept
-                // in TMEM in between: the unrolled row had its instructions fetched anew each time.
-                uint32_t a[32];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t in = 0;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            in |= ((there >> ((h * 32 + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
+                        see[h] = in & (bit_range(low, pos + 1, j0 + 32 * h) | bit_range(0, min(p.sinks, pos + 1), j0 + 32 * h));
+                    }
+                }
+                uint32_t a[2][32];   // logits over row_f, then weights (fp32)
+                tmem_ld_32x32b_x32(s_addr + b * 64u, a[0]);
+                tmem_ld_32x32b_x32(s_addr + b * 64u + 32u, a[1]);
+                tmem_ld_wait();
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int32_t c = 0; c < 64; c += 32) {
-                    tmem_ld_32x32b_x32(s_addr + c, a);
-                    tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 k4 = lds_v4(skb + (c + e) * 4);   // a broadcast
+                        const float4 k4 = lds_v4(skb + (h * 32 + e) * 4);   // a broadcast
                         // fp32(acc) without the conversion pipe (attention.cuh), times s_k
                         float f[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            f[u] = __uint_as_float(a[e + u] + 0x4B400000u);
+                            f[u] = __uint_as_float(a[h][e + u] + 0x4B400000u);
                         sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
                         sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
                         mul2(f[0], f[1], f[0], f[1], k4.x, k4.y);
                         mul2(f[2], f[3], f[2], f[3], k4.z, k4.w);
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            a[e + u] = __float_as_uint(f[u]);
+                            a[h][e + u] = __float_as_uint(f[u]);
                     }
                     if (!whole) {
-                        const uint32_t see = visible(c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            a[e] = (see >> e) & 1u ? a[e] : 0xff800000u;   // -inf
+                            a[h][e] = (see[h] >> e) & 1u ? a[h][e] : 0xff800000u;   // -inf
                     }
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            mx[u] = max3f(mx[u], __uint_as_float(a[e + u]), __uint_as_float(a[e + u + 4]));
-                    tmem_st_32x32b_x32(s_addr + c, a);
+                            mx[u] = max3f(mx[u], __uint_as_float(a[h][e + u]), __uint_as_float(a[h][e + u + 4]));
                 }
-                tmem_st_wait();
-                float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
-                // the sums are rescaled only when a row's maximum, over both halves, grows by more
-                // than 8 (weights stay below 2^8 s_v)
-                const bool any_grow = bar_sync_or(pair_bar, 64, mb > m_used + 8.0f);
-                float alpha = 1.0f;
-                if (any_grow) {
-                    mb = fmaxf(mb, swap(mb));
-                    const bool grow = mb > m_used + 8.0f;
-                    alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
+                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
+                // the sums are rescaled only when the maximum grows by more than 8 (weights stay
+                // below 2^8 s_v); O is stable once the product of the step before is done
+                const bool grow = mb > m_used + 8.0f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
+                    if (k > 0) {
+                        wait(pv_done(tile, b ^ 1u), ((g - 1u) >> 1) & 1u);
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int32_t c = 0; c < D; c += 16) {
+                            uint32_t x[16];
+                            tmem_ld_32x32b_x16(o_addr + c, x);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const uint32_t y[4] = {x[e], x[e + 1], x[e + 2], x[e + 3]};
+                                tmem_st_32x32b_x4(o_addr + c + e, y);
+                            }
+                        }
+                        tmem_st_wait();
+                    }
                 }
-                // tile 0 runs its exponentials of a key tile after tile 1 ran those of the one
-                // before, tile 1 after tile 0 ran those of the same one
-                wait(turn(tile), (blocks & 1u) ^ (tile ^ 1u));
-                // P = 2^(y - m) s_v, bf16, into the swizzled K-major tile (attention.cuh)
+                // P = 2^(y - m) s_v, bf16, into this buffer's swizzled K-major tile (attention.cuh)
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0, 0, 0, 0};
-#pragma unroll 1
-                for (int32_t c = 0; c < 64; c += 32) {
-                    tmem_ld_32x32b_x32(s_addr + c, a);
-                    tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const float4 v4 = lds_v4(skb + 512u + (c + e) * 4);
+                        const float4 v4 = lds_v4(skb + 256u + (h * 32 + e) * 4);
                         float f[4];
-                        fma2(f[0], f[1], __uint_as_float(a[e]), __uint_as_float(a[e + 1]), row_f, row_f, neg_m, neg_m);
-                        fma2(f[2], f[3], __uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]), row_f, row_f, neg_m, neg_m);
+                        fma2(f[0], f[1], __uint_as_float(a[h][e]), __uint_as_float(a[h][e + 1]), row_f, row_f, neg_m, neg_m);
+                        fma2(f[2], f[3], __uint_as_float(a[h][e + 2]), __uint_as_float(a[h][e + 3]), row_f, row_f, neg_m, neg_m);
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
                             f[u] = ex2_approx(f[u]);
@@ -701,109 +651,92 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            a[e + u] = __float_as_uint(f[u]);
+                            a[h][e + u] = __float_as_uint(f[u]);
                     }
                     if (!whole) {   // a hidden key adds 0 whatever its scale holds
-                        const uint32_t see = visible(c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            a[e] = (see >> e) & 1u ? a[e] : 0u;
+                            a[h][e] = (see[h] >> e) & 1u ? a[h][e] : 0u;
                     }
-                    // the P tile is free, and O stable, once the tile's last product is done
-                    if (c == 0 && k > 0) {
-                        wait(pv_done(tile), (mine & 1u) ^ 1u);
-                        tc_fence_after_sync();
-                    }
+                    if (h == 0)   // the P buffer is free once the product of two steps before is done
+                        wait(pv_done(tile, b), ph ^ 1u);
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) {
                         uint32_t x[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[8 * ch + 2 * u]),
-                                                                            __uint_as_float(a[8 * ch + 2 * u + 1]));
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[h][8 * ch + 2 * u]),
+                                                                            __uint_as_float(a[h][8 * ch + 2 * u + 1]));
                             x[u] = *reinterpret_cast<const uint32_t *>(&h2);
                         }
-                        const uint32_t c16 = static_cast<uint32_t>((c >> 3) + ch) ^ (static_cast<uint32_t>(r) & 7u);
-                        sts_v4(prow + (c16 << 4), x[0], x[1], x[2], x[3]);
+                        const uint32_t c16 = static_cast<uint32_t>(h * 4 + ch) ^ (static_cast<uint32_t>(r) & 7u);
+                        sts_v4(prow + b * C::P_BUF + (c16 << 4), x[0], x[1], x[2], x[3]);
                     }
                 }
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(turn(tile ^ 1u));
+                    mbar_arrive(p_full(tile, b));
                     mbar_arrive(sc_empty(ss));
                 }
                 if (++ss == NS)
                     ss = 0, sph ^= 1u;
-                if (any_grow && k > 0) {   // this half's columns of O
-#pragma unroll 1
-                    for (int32_t c = 0; c < D / 2; c += 32) {
-                        tmem_ld_32x32b_x32(o_addr + half * (D / 2) + c, a);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            a[e] = __float_as_uint(__uint_as_float(a[e]) * alpha);
-                        tmem_st_32x32b_x32(o_addr + half * (D / 2) + c, a);
-                    }
-                    tmem_st_wait();
-                }
-                fence_proxy_async_smem();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(p_full(tile));
-                ++mine;
             }
-            const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
-            wait(pv_done(tile), (mine & 1u) ^ 1u);
+            const bool begins = w.i == 0, ends = w.i + steps == w.t.nt, finish = begins && ends;
+            wait(pv_done(tile, (g - 1u) & 1u), ((g - 1u) >> 1) & 1u);
             tc_fence_after_sync();
-            l_sum += swap(l_sum);
-            // this half's columns of O. A whole segment's are un-rotated first: the last stage of a
-            // group of D joins the two halves, so that each thread has its own columns after it
-            const bool finish = begins && ends, join = finish && p.group == D;
-            float v[D / 2];
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t x[32], y[32];
-                tmem_ld_32x32b_x32(o_addr + half * (D / 2) + c * 32, x);
-                tmem_ld_32x32b_x32(o_addr + (half ^ 1u) * (D / 2) + c * 32, y);
-                tmem_ld_wait();
+            // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
+            // D joins the halves, first, and each half has its own stages after that.
+            const bool join = finish && p.group == D;
+            const float inv = l_sum == 0.0f ? 0.0f : __fdiv_rn(kCodeUnit * p.c_g, l_sum);
+            const int32_t head = w.kvh * p.share + r0 + lr - tok * p.share;   // (of a row in use)
+            uint16_t *o = p.o + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(head) * D;
+            float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
+#pragma unroll 1
+            for (int32_t half = 0; half < 2; ++half) {
                 const float own = half ? -1.0f : 1.0f;
+                float v[D / 2];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[c * 32 + e] = join ? __fmaf_rn(__uint_as_float(x[e]), own, __uint_as_float(y[e])) : __uint_as_float(x[e]);
+                for (int c = 0; c < D / 2; c += 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld_32x32b_x16(o_addr + half * (D / 2) + c, x);
+                    tmem_ld_32x32b_x16(o_addr + (half ^ 1) * (D / 2) + c, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[c + e] = join ? __fmaf_rn(__uint_as_float(x[e]), own, __uint_as_float(y[e])) : __uint_as_float(x[e]);
+                }
+                if (finish) {
+                    thread_butterfly<D / 2>(v, p.group);
+                    if (ok && lr < rows) {
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * e + 2 * u] * inv, v[8 * e + 2 * u + 1] * inv);
+                                x[u] = *reinterpret_cast<const uint32_t *>(&h2);
+                            }
+                            st_v4(o + half * (D / 2) + 8 * e, x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                } else if (lr < rows) {
+#pragma unroll
+                    for (int e = 0; e < D / 8; ++e)
+                        *reinterpret_cast<float4 *>(ws + lr * D + half * (D / 2) + 4 * e) =
+                            make_float4(v[4 * e] * kCodeUnit, v[4 * e + 1] * kCodeUnit, v[4 * e + 2] * kCodeUnit,
+                                        v[4 * e + 3] * kCodeUnit);
+                }
             }
             tc_fence_before_sync();
-            if (finish) {
-                thread_butterfly<D / 2>(v, p.group);
-                const float inv = l_sum == 0.0f ? 0.0f : __fdiv_rn(kCodeUnit * p.c_g, l_sum);
-                const int32_t head = w.kvh * p.share + r0 + lr - tok * p.share;   // (of a row in use)
-                uint16_t *o = p.o + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(head) * D + half * (D / 2);
-                if (ok && lr < rows) {
-#pragma unroll
-                    for (int e = 0; e < D / 16; ++e) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * e + 2 * u] * inv, v[8 * e + 2 * u + 1] * inv);
-                            x[u] = *reinterpret_cast<const uint32_t *>(&h2);
-                        }
-                        st_v4(o + 8 * e, x[0], x[1], x[2], x[3]);
-                    }
-                }
-            } else if (lr < rows) {
-                float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
-#pragma unroll
-                for (int e = 0; e < D / 8; ++e)
-                    *reinterpret_cast<float4 *>(ws + lr * D + half * (D / 2) + 4 * e) =
-                        make_float4(v[4 * e] * kCodeUnit, v[4 * e + 1] * kCodeUnit, v[4 * e + 2] * kCodeUnit,
-                                    v[4 * e + 3] * kCodeUnit);
-                if (half == 0u)
-                    *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, l_sum);
-            }
-            n += tiles;
+            if (!finish && lr < rows)
+                *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, l_sum);
+            n += steps;
             if (threadIdx.x == 128 && begins && !ends) {
-                const int64_t end = first + n - tiles + w.t.nt - 1;
+                // the segment's last step is nt - steps further on: that many blocks hold pieces
+                const int64_t end = first + n - steps + w.t.nt - 1;
                 desc->pieces = static_cast<int32_t>(end / per) - static_cast<int32_t>(blockIdx.x) + 1;
                 desc->q0 = w.s.q0;
                 desc->rows = rows;

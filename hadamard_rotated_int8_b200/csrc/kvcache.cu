@@ -170,7 +170,7 @@ sdnq_status launch_chunk(const PagedParams &p, const DeviceInfo &dev, int sms, c
     using C = ChunkConfig<D>;
     CUtensorMap map;
     const uint32_t page = 1u << p.page_shift;
-    if (!make_pool_map<D>(&map, p, page <= kChunkBox ? page : kChunkBox))
+    if (!make_pool_map<D>(&map, p, page <= kChunkTile ? page : kChunkTile))
         return SDNQ_ERR_CUDA;
     static PerDeviceCache<1> smem;
     if (!smem_attr_once(smem, dev.index, attn_chunk_kernel<D>, C::SMEM_BYTES)) {
