@@ -28,7 +28,7 @@ constexpr int kChunkThreads = 384;
 
 template <int D>
 struct ChunkConfig {
-    static constexpr int NK = 4, NV = 3, NB = 4, NS = 6;   // stages: K, value codes, bf16 values, scales
+    static constexpr int NK = 4, NV = 3, NB = 4, NS = 8;   // stages: K, value codes, bf16 values, scales
     static constexpr int Q_TILE = 128 * D, K_STAGE = 64 * D, V_STAGE = 64 * D, B_STAGE = 64 * D * 2;
     static constexpr int P_BUF = 128 * 64 * 2;
     static constexpr int Q_OFF = 0;
@@ -39,8 +39,8 @@ struct ChunkConfig {
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 64 key scales, 64 value scales a stage
     static constexpr int QS_OFF = SC_OFF + NS * 512;        // query scales
     static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
-    // full and empty of each ring, then per tile and buffer s_full, p_full, pv_done; q_full; drain
-    static constexpr int NBARS = 2 * (NK + NV + NB + NS) + 12 + 2 + 1;
+    // full and empty of each ring (the scales come with the keys), then per tile and buffer s_full, p_full, pv_done; q_full; drain
+    static constexpr int NBARS = 2 * (NK + NV + NB) + NS + 12 + 2 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
     static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
@@ -204,10 +204,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto v_empty = [&](uint32_t s) { return bar0 + 8u * (2 * NK + NV + s); };
     auto b_full = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV) + s); };
     auto b_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV) + NB + s); };
-    auto sc_full = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + s); };
-    auto sc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + NS + s); };
+    auto sc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + s); };
     // per tile t and buffer b, one phase every other step: S written, P written, P V done
-    constexpr int TB = 2 * (NK + NV + NB + NS);
+    constexpr int TB = 2 * (NK + NV + NB) + NS;
     auto s_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 2 * t + b); };
     auto p_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 4 + 2 * t + b); };
     auto pv_done = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 8 + 2 * t + b); };
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int s = 0; s < NB; ++s)
             mbar_init(b_full(s), 2), mbar_init(b_empty(s), 1);
         for (int s = 0; s < NS; ++s)
-            mbar_init(sc_full(s), 1), mbar_init(sc_empty(s), 8);
+            mbar_init(sc_empty(s), 8);
         for (int t = 0; t < 2; ++t) {
             for (int b = 0; b < 2; ++b)
                 mbar_init(s_full(t, b), 1), mbar_init(p_full(t, b), 4), mbar_init(pv_done(t, b), 1);
@@ -270,6 +269,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
         return ok;
+    };
+    auto wait_lane = [&](uint32_t bar, uint32_t parity) {   // where nothing hangs on the lanes' agreement
+        if (ok)
+            ok = mbar_wait_tries(bar, parity, abort);
+        __syncwarp();
     };
 
     if (warp == 0) {
@@ -319,8 +323,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     break;
                 if (lane == 0) {
                     meta[ss] = valid;
-                    mbar_arrive_expect_tx(k_full(ks), keys * D);
-                    mbar_arrive_expect_tx(sc_full(ss), keys * 8u);
+                    mbar_arrive_expect_tx(k_full(ks), keys * (D + 8u));
                     mbar_arrive_expect_tx(v_full(vs), keys * D);
                 }
                 __syncwarp();
@@ -328,8 +331,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (mine) {
                     tma_load_2d(base + C::K_OFF + ks * C::K_STAGE + lane * pp * D, &tmPool, k_full(ks), 0, krow);
                     const uint32_t sdst = base + C::SC_OFF + ss * 512u + lane * pp * 4u;
-                    bulk_load_1d(sdst, p.scales + krow, 4u * pp, sc_full(ss));
-                    bulk_load_1d(sdst + 256u, p.scales + vrow, 4u * pp, sc_full(ss));
+                    bulk_load_1d(sdst, p.scales + krow, 4u * pp, k_full(ks));
+                    bulk_load_1d(sdst + 256u, p.scales + vrow, 4u * pp, k_full(ks));
                     tma_load_2d(base + C::V_OFF + vs * C::V_STAGE + lane * pp * D, &tmPool, v_full(vs), 0, vrow);
                 }
                 if (++ks == NK)
@@ -349,7 +352,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 mbar_wait_tries(bar + 8u * static_cast<uint32_t>(j % stages), static_cast<uint32_t>(j / stages) & 1u, abort);
         };
         drain(k_full(0), NK);
-        drain(sc_full(0), NS);
         drain(v_full(0), NV);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
@@ -470,20 +472,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u;
         const uint32_t o_addr = s_addr + 256u;
         const uint32_t prow = base + C::P_OFF + tile * 2u * C::P_BUF + static_cast<uint32_t>(r) * 128u;
-        uint32_t ss = 0, sph = 0, g = 0;   // scale ring; steps of this tile
+        uint32_t g = 0;        // steps of this tile
         bool open = false;
         int64_t n = 0;
         while (n < count) {
             const int32_t steps = piece_steps(n), rows = piece_rows(), r0 = w.q * kChunkRows;
-            if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile: it only hands the scales on
-#pragma unroll 1
-                for (int32_t k = 0; k < steps; ++k) {
-                    wait(sc_full(ss), sph);
-                    if (lane == 0)
-                        mbar_arrive(sc_empty(ss));
-                    if (++ss == NS)
-                        ss = 0, sph ^= 1u;
-                }
+            const uint32_t n0 = static_cast<uint32_t>(n);
+            if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile: its part in freeing the scales
+                if (lane == 0)
+                    for (int32_t k = 0; k < steps; ++k) {
+                        ok = ok && mbar_wait_tries(sc_empty((n0 + k) % NS), (((n0 + k) / NS) & 1u) ^ 1u, abort);
+                        mbar_arrive(sc_empty((n0 + k) % NS));
+                    }
+                __syncwarp();
                 n += steps;
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
@@ -547,127 +548,139 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (lane == 0)
                 mbar_arrive(q_full(tile));
             float m_used = -INFINITY, l_sum = 0.0f;
-#pragma unroll 1
-            for (int32_t k = 0; k < steps; ++k, ++g) {
-                const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
+            uint32_t see[2] = {0u, 0u};   // visible columns of a step: [low, pos] and the sinks, in pages that are there
+            auto look = [&](int32_t k) {
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
-                const uint32_t skb = base + C::SC_OFF + ss * 512u;
-                wait(s_full(tile, b), ph);
-                wait(sc_full(ss), sph);
-                tc_fence_after_sync();
-                const uint32_t there = meta[ss];
-                const bool whole = j0 + 63 <= pos_first && (j0 >= low_last || j0 + 64 <= p.sinks) && there == all_boxes;
-                uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-                if (!whole) {   // visible columns: [low, pos] and the sinks, in pages that are there
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t in = 0;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            in |= ((there >> ((h * 32 + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
-                        see[h] = in & (bit_range(low, pos + 1, j0 + 32 * h) | bit_range(0, min(p.sinks, pos + 1), j0 + 32 * h));
-                    }
-                }
-                uint32_t a[2][32];   // logits over row_f, then weights (fp32)
-                tmem_ld_32x32b_x32(s_addr + b * 64u, a[0]);
-                tmem_ld_32x32b_x32(s_addr + b * 64u + 32u, a[1]);
-                tmem_ld_wait();
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const uint32_t there = meta[(n0 + k) % NS];
+                if (j0 + 63 <= pos_first && (j0 >= low_last || j0 + 64 <= p.sinks) && there == all_boxes)
+                    return true;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    uint32_t in = 0;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 k4 = lds_v4(skb + (h * 32 + e) * 4);   // a broadcast
-                        // fp32(acc) without the conversion pipe (attention.cuh), times s_k
-                        float f[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            f[u] = __uint_as_float(a[h][e + u] + 0x4B400000u);
-                        sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
-                        sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
-                        mul2(f[0], f[1], f[0], f[1], k4.x, k4.y);
-                        mul2(f[2], f[3], f[2], f[3], k4.z, k4.w);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            a[h][e + u] = __float_as_uint(f[u]);
-                    }
-                    if (!whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            a[h][e] = (see[h] >> e) & 1u ? a[h][e] : 0xff800000u;   // -inf
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            mx[u] = max3f(mx[u], __uint_as_float(a[h][e + u]), __uint_as_float(a[h][e + u + 4]));
+                    for (int u = 0; u < 2; ++u)
+                        in |= ((there >> ((h * 32 + u * 16) >> pp_shift)) & 1u) ? 0xffffu << (16 * u) : 0u;
+                    see[h] = in & (bit_range(low, pos + 1, j0 + 32 * h) | bit_range(0, min(p.sinks, pos + 1), j0 + 32 * h));
                 }
-                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
+                return false;
+            };
+            // acc * s_k of 4 columns; fp32(acc) without the conversion pipe (attention.cuh)
+            auto scale4 = [&](const uint32_t *acc, float *y, uint32_t at) {
+                const float4 k4 = lds_v4(at);   // a broadcast
+                float f[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    f[u] = __uint_as_float(acc[u] + 0x4B400000u);
+                sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
+                sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
+                mul2(y[0], y[1], f[0], f[1], k4.x, k4.y);
+                mul2(y[2], y[3], f[2], f[3], k4.z, k4.w);
+            };
+            float y[64] = {};   // logits over row_f of the step at hand
+            auto top = [&] {
+                float mx[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                    for (int e = 4; e < 60; e += 8)
+                        mx[u] = max3f(mx[u], y[e + u], y[e + u + 4]);
+                    mx[u] = fmaxf(mx[u], y[60 + u]);
+                }
+                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * row_f;
+            };
+            auto hide = [&] {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    y[e] = (see[e >> 5] >> (e & 31)) & 1u ? y[e] : -INFINITY;
+            };
+            // The loop handles a step's exponentials together with the scaling of the next one's
+            // logits, column by column in the same registers: the two use different pipes.
+            uint32_t acc[32];
+            wait_lane(s_full(tile, g & 1u), (g >> 1) & 1u);
+            tc_fence_after_sync();
+            bool whole = look(0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                tmem_ld_32x32b_x32(s_addr + (g & 1u) * 64u + h * 32u, acc);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NS) * 512u + (h * 32 + e) * 4);
+            }
+            if (!whole)
+                hide();
+#pragma unroll 1
+            for (int32_t k = 0; k < steps; ++k, ++g) {
+                const uint32_t b = g & 1u, ph = (g >> 1) & 1u, ss = (n0 + k) % NS;
+                const uint32_t svb = base + C::SC_OFF + ss * 512u + 256u;
+                const uint32_t skb = base + C::SC_OFF + ((n0 + k + 1) % NS) * 512u;
+                const bool more = k + 1 < steps;
                 // the sums are rescaled only when the maximum grows by more than 8 (weights stay
                 // below 2^8 s_v); O is stable once the product of the step before is done
+                const float mb = top();
                 const bool grow = mb > m_used + 8.0f;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
                     if (k > 0) {
-                        wait(pv_done(tile, b ^ 1u), ((g - 1u) >> 1) & 1u);
+                        wait_lane(pv_done(tile, b ^ 1u), ((g - 1u) >> 1) & 1u);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int32_t c = 0; c < D; c += 16) {
-                            uint32_t x[16];
-                            tmem_ld_32x32b_x16(o_addr + c, x);
+                        for (int32_t c = 0; c < D; c += 32) {
+                            tmem_ld_32x32b_x32(o_addr + c, acc);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const uint32_t y[4] = {x[e], x[e + 1], x[e + 2], x[e + 3]};
-                                tmem_st_32x32b_x4(o_addr + c + e, y);
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                acc[e] = __float_as_uint(__uint_as_float(acc[e]) * alpha);
+                            tmem_st_32x32b_x32(o_addr + c, acc);
                         }
                         tmem_st_wait();
                     }
                 }
+                // the P buffer is free once the product of two steps before is done
+                wait_lane(pv_done(tile, b), ph ^ 1u);
+                if (more)
+                    wait_lane(s_full(tile, b ^ 1u), ((g + 1u) >> 1) & 1u);
+                tc_fence_after_sync();
+                const bool was_whole = whole;
+                const uint32_t saw[2] = {see[0], see[1]};
+                if (more)
+                    whole = look(k + 1);
                 // P = 2^(y - m) s_v, bf16, into this buffer's swizzled K-major tile (attention.cuh)
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 v4 = lds_v4(skb + 256u + (h * 32 + e) * 4);
-                        float f[4];
-                        fma2(f[0], f[1], __uint_as_float(a[h][e]), __uint_as_float(a[h][e + 1]), row_f, row_f, neg_m, neg_m);
-                        fma2(f[2], f[3], __uint_as_float(a[h][e + 2]), __uint_as_float(a[h][e + 3]), row_f, row_f, neg_m, neg_m);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            f[u] = ex2_approx(f[u]);
-                        add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
-                        add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
-                        mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
-                        mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            a[h][e + u] = __float_as_uint(f[u]);
-                    }
-                    if (!whole) {   // a hidden key adds 0 whatever its scale holds
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            a[h][e] = (see[h] >> e) & 1u ? a[h][e] : 0u;
-                    }
-                    if (h == 0)   // the P buffer is free once the product of two steps before is done
-                        wait(pv_done(tile, b), ph ^ 1u);
+                    tmem_ld_32x32b_x32(s_addr + (b ^ 1u) * 64u + h * 32u, acc);   // (of the last step: not used)
+                    tmem_ld_wait();
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) {
                         uint32_t x[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(a[h][8 * ch + 2 * u]),
-                                                                            __uint_as_float(a[h][8 * ch + 2 * u + 1]));
-                            x[u] = *reinterpret_cast<const uint32_t *>(&h2);
+                        for (int q = 0; q < 2; ++q) {
+                            float *z = y + h * 32 + ch * 8 + q * 4;
+                            const float4 v4 = lds_v4(svb + (h * 32 + ch * 8 + q * 4) * 4);
+                            float f[4];
+                            fma2(f[0], f[1], z[0], z[1], row_f, row_f, neg_m, neg_m);
+                            fma2(f[2], f[3], z[2], z[3], row_f, row_f, neg_m, neg_m);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                f[u] = ex2_approx(f[u]);
+                            scale4(acc + ch * 8 + q * 4, z, skb + (h * 32 + ch * 8 + q * 4) * 4);
+                            add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
+                            add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
+                            mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
+                            mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
+                            if (!was_whole) {   // a hidden key adds 0 whatever its scale holds
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    f[u] = (saw[h] >> (ch * 8 + q * 4 + u)) & 1u ? f[u] : 0.0f;
+                            }
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+                            x[2 * q] = *reinterpret_cast<const uint32_t *>(&lo);
+                            x[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&hi);
                         }
                         const uint32_t c16 = static_cast<uint32_t>(h * 4 + ch) ^ (static_cast<uint32_t>(r) & 7u);
                         sts_v4(prow + b * C::P_BUF + (c16 << 4), x[0], x[1], x[2], x[3]);
@@ -681,11 +694,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     mbar_arrive(p_full(tile, b));
                     mbar_arrive(sc_empty(ss));
                 }
-                if (++ss == NS)
-                    ss = 0, sph ^= 1u;
+                if (more && !whole)
+                    hide();
             }
             const bool begins = w.i == 0, ends = w.i + steps == w.t.nt, finish = begins && ends;
-            wait(pv_done(tile, (g - 1u) & 1u), ((g - 1u) >> 1) & 1u);
+            wait_lane(pv_done(tile, (g - 1u) & 1u), ((g - 1u) >> 1) & 1u);
             tc_fence_after_sync();
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
