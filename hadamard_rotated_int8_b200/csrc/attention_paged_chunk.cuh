@@ -8,8 +8,10 @@
 //   128-byte-swizzled operand of the second product;
 // - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) two steps ahead of
 //   O_t += P_t V (kind::f16, fp32 in TMEM): logits and P of a tile have two buffers each, so
-//   that its softmax never waits for a product just issued (128-key steps with one buffer
-//   spent 3500 cycles a step in hand-overs alone);
+//   that its softmax never waits for a product just issued. A commit costs the issuing warp
+//   about 200 cycles and a wait 110 or more, so there is one commit a tile and step: `done` of
+//   iteration k covers S(k) and P(k - 2) V(k - 2), and everything else follows from the
+//   softmax's "P written": K(k) and its scales may be replaced, P(k - 1) V(k - 1) is done;
 // - warps 4..7 (tile 0) and 8..11 (tile 1), one thread a query row, rotate and quantize their
 //   query rows into the operand tile, then per step form 64 base-2 logits, an online softmax
 //   (sums rescaled only when the maximum grows by more than 8), and P = probability * s_v in
@@ -28,7 +30,7 @@ constexpr int kChunkThreads = 384;
 
 template <int D>
 struct ChunkConfig {
-    static constexpr int NK = 4, NV = 3, NB = 4, NS = 8;   // stages: K, value codes, bf16 values, scales
+    static constexpr int NK = 4, NV = 3, NB = 4;   // stages: K and scales, value codes, bf16 values
     static constexpr int Q_TILE = 128 * D, K_STAGE = 64 * D, V_STAGE = 64 * D, B_STAGE = 64 * D * 2;
     static constexpr int P_BUF = 128 * 64 * 2;
     static constexpr int Q_OFF = 0;
@@ -37,13 +39,14 @@ struct ChunkConfig {
     static constexpr int B_OFF = K_OFF + NK * K_STAGE;
     static constexpr int V_OFF = B_OFF + NB * B_STAGE;
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 64 key scales, 64 value scales a stage
-    static constexpr int QS_OFF = SC_OFF + NS * 512;        // query scales
+    static constexpr int QS_OFF = SC_OFF + NK * 512;        // query scales
     static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
-    // full and empty of each ring (the scales come with the keys), then per tile and buffer s_full, p_full, pv_done; q_full; drain
-    static constexpr int NBARS = 2 * (NK + NV + NB) + NS + 12 + 2 + 1;
-    static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
-    static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
+    // full and empty of each ring, then per tile and buffer done and p_full; q_full; drain
+    static constexpr int NBARS = 2 * (NK + NV + NB) + 8 + 2 + 1;
+    static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each K stage
+    static constexpr int HOLD_OFF = META_OFF + NK * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
+    static_assert((NK & (NK - 1)) == 0 && (NB & (NB - 1)) == 0, "ring positions are masked");
     static constexpr int64_t PIECE = static_cast<int64_t>(kChunkRows) * (D + 2);   // floats, as FewConfig's
     static_assert(SMEM_BYTES + 256 <= 232448, "shared memory per block");
 };
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ CUtensorMap tmPool, const PagedParams p)
 {
     using C = ChunkConfig<D>;
-    constexpr int NK = C::NK, NV = C::NV, NB = C::NB, NS = C::NS;
+    constexpr int NK = C::NK, NV = C::NV, NB = C::NB;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -204,14 +207,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     auto v_empty = [&](uint32_t s) { return bar0 + 8u * (2 * NK + NV + s); };
     auto b_full = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV) + s); };
     auto b_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV) + NB + s); };
-    auto sc_empty = [&](uint32_t s) { return bar0 + 8u * (2 * (NK + NV + NB) + s); };
-    // per tile t and buffer b, one phase every other step: S written, P written, P V done
-    constexpr int TB = 2 * (NK + NV + NB) + NS;
-    auto s_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 2 * t + b); };
+    // per tile t and buffer b: iteration done, P written (one phase every other step)
+    constexpr int TB = 2 * (NK + NV + NB);
+    auto done = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 2 * t + b); };
     auto p_full = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 4 + 2 * t + b); };
-    auto pv_done = [&](uint32_t t, uint32_t b) { return bar0 + 8u * (TB + 8 + 2 * t + b); };
-    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 12 + t); };
-    const uint32_t drain_bar = bar0 + 8u * (TB + 14);
+    auto q_full = [&](uint32_t t) { return bar0 + 8u * (TB + 8 + t); };
+    const uint32_t drain_bar = bar0 + 8u * (TB + 10);
     volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(smem + C::META_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -225,11 +226,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(v_full(s), 1), mbar_init(v_empty(s), 2);
         for (int s = 0; s < NB; ++s)
             mbar_init(b_full(s), 2), mbar_init(b_empty(s), 1);
-        for (int s = 0; s < NS; ++s)
-            mbar_init(sc_empty(s), 8);
         for (int t = 0; t < 2; ++t) {
             for (int b = 0; b < 2; ++b)
-                mbar_init(s_full(t, b), 1), mbar_init(p_full(t, b), 4), mbar_init(pv_done(t, b), 1);
+                mbar_init(done(t, b), 1), mbar_init(p_full(t, b), 4);
             mbar_init(q_full(t), 4);
         }
         mbar_init(drain_bar, 1);
@@ -264,21 +263,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t all_boxes = (1u << nbox) - 1u;
     auto piece_steps = [&](int64_t n) { return static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n)); };
     auto piece_rows = [&] { return min(kChunkRows, w.s.n * p.share - w.q * kChunkRows); };
-    // A role that gave up waiting runs its loops to their end without waiting or storing.
+    // A role that gave up waiting runs its loops to their end without waiting or storing (the
+    // loader stops loading).
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_tries(bar, parity, abort));
-        return ok;
-    };
-    auto wait_lane = [&](uint32_t bar, uint32_t parity) {   // where nothing hangs on the lanes' agreement
-        if (ok)
+        if (ok && !mbar_try_wait(bar, parity))
             ok = mbar_wait_tries(bar, parity, abort);
+        __syncwarp();
+    };
+    auto wait2 = [&](uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2) {   // the tries overlap
+        const bool a = mbar_try_wait(bar, parity), b = mbar_try_wait(bar2, parity2);
+        if (ok && !a)
+            ok = mbar_wait_tries(bar, parity, abort);
+        if (ok && !b)
+            ok = mbar_wait_tries(bar2, parity2, abort);
         __syncwarp();
     };
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        uint32_t ks = 0, kph = 1, vs = 0, vph = 1, ss = 0, sph = 1;
+        uint32_t ks = 0, kph = 1, vs = 0, vph = 1;
         int64_t n = 0, issued = 0;
         while (ok && n < count) {
             const int32_t steps = piece_steps(n);
@@ -319,10 +323,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                                 (j & ((1 << p.page_shift) - 1))
                                           : 0;
                 const int32_t vrow = krow + (1 << p.page_shift);
-                if (!wait(k_empty(ks), kph) || !wait(sc_empty(ss), sph) || !wait(v_empty(vs), vph))
+                wait2(k_empty(ks), kph, v_empty(vs), vph);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
                 if (lane == 0) {
-                    meta[ss] = valid;
+                    meta[ks] = valid;
                     mbar_arrive_expect_tx(k_full(ks), keys * (D + 8u));
                     mbar_arrive_expect_tx(v_full(vs), keys * D);
                 }
@@ -330,15 +336,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ++issued;
                 if (mine) {
                     tma_load_2d(base + C::K_OFF + ks * C::K_STAGE + lane * pp * D, &tmPool, k_full(ks), 0, krow);
-                    const uint32_t sdst = base + C::SC_OFF + ss * 512u + lane * pp * 4u;
+                    const uint32_t sdst = base + C::SC_OFF + ks * 512u + lane * pp * 4u;
                     bulk_load_1d(sdst, p.scales + krow, 4u * pp, k_full(ks));
                     bulk_load_1d(sdst + 256u, p.scales + vrow, 4u * pp, k_full(ks));
                     tma_load_2d(base + C::V_OFF + vs * C::V_STAGE + lane * pp * D, &tmPool, v_full(vs), 0, vrow);
                 }
                 if (++ks == NK)
                     ks = 0, kph ^= 1u;
-                if (++ss == NS)
-                    ss = 0, sph ^= 1u;
                 if (++vs == NV)
                     vs = 0, vph ^= 1u;
             }
@@ -363,31 +367,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // operand descriptors; 16 bytes further on is 1 more
         const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
         const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
-        uint32_t ks = 0, kph = 0, bs = 0, bph = 0;
-        uint32_t g0 = 0, g1 = 0, q_n = 0;   // steps of tiles 0 and 1 before this piece; bit t: tile t's pieces, mod 2
+        // steps of all pieces so far; steps of each tile's pieces, and these pieces
+        uint32_t c0 = 0, g0 = 0, g1 = 0, n_p0 = 0, n_p1 = 0;
         int64_t n = 0;
-        while (ok && n < count) {
+        while (n < count) {
             const int32_t steps = piece_steps(n);
             const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
-            // S_t of step k goes out when P_t of step k - 2 is written (that S buffer has been
-            // read then), just before the product of that P with V
+            // iteration k: S of step k goes out when P of step k - 2 is written (that S buffer has
+            // been read then), just before the product of that P with V
 #pragma unroll 1
-            for (int32_t k = 0; ok && k < steps + 2; ++k) {
-                if (k < steps)
-                    wait(k_full(ks), kph);
-                if (k >= 2)
-                    wait(b_full(bs), bph);
+            for (int32_t k = 0; k < steps + 2; ++k) {
+                const uint32_t c = c0 + static_cast<uint32_t>(k), ks = c % NK, bs = (c - 2u) % NB;   // ring positions
+                if (k >= 2 && k < steps)
+                    wait2(k_full(ks), (c / NK) & 1u, b_full(bs), ((c - 2u) / NB) & 1u);
+                else if (k < steps)
+                    wait(k_full(ks), (c / NK) & 1u);
+                else if (k >= 2)
+                    wait(b_full(bs), ((c - 2u) / NB) & 1u);
 #pragma unroll 1
                 for (uint32_t t = 0; t < in_use; ++t) {
-                    const uint32_t g = (t == 0 ? g0 : g1) + static_cast<uint32_t>(k), b = g & 1u;   // step k, and k - 2's buffers
-                    if (k == 0) {
-                        wait(q_full(t), (q_n >> t) & 1u);
-                        q_n ^= 1u << t;
-                    }
+                    const uint32_t g = (t == 0 ? g0 : g1) + static_cast<uint32_t>(k), b = g & 1u;
                     if (k >= 2)
                         wait(p_full(t, b), ((g >> 1) & 1u) ^ 1u);
-                    if (!ok)
-                        break;
+                    else if (k == 0)
+                        wait(q_full(t), (t == 0 ? n_p0 : n_p1) & 1u);
                     tc_fence_after_sync();
                     const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
                     const uint64_t pa = dp + (2 * t + b) * (C::P_BUF >> 4), va = db + bs * (C::B_STAGE >> 4);
@@ -396,28 +399,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
                                 mma_s8(tmem_base + t * 128 + b * 64, qa + 2 * kk, ka + 2 * kk, IDESC_S, kk != 0 ? 1u : 0u);
-                            tc_commit(s_full(t, b));
-                            if (t + 1 == in_use)
-                                tc_commit(k_empty(ks));
                         }
                         if (k >= 2) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, k > 2 || kk != 0 ? 1u : 0u);
-                            tc_commit(pv_done(t, b));
-                            if (t + 1 == in_use)
-                                tc_commit(b_empty(bs));
                         }
+                        tc_commit(done(t, b));
                     }
                     __syncwarp();
                 }
-                if (k < steps && ++ks == NK)
-                    ks = 0, kph ^= 1u;
-                if (k >= 2 && ++bs == NB)
-                    bs = 0, bph ^= 1u;
+                if (leader) {
+                    if (k >= 2)       // every P of step k - 2 is written: its K and scales are read
+                        mbar_arrive(k_empty((c - 2u) % NK));
+                    if (k >= 3)       // and its writers saw the product of step k - 3 done
+                        mbar_arrive(b_empty((c - 3u) % NB));
+                    if (k == steps + 1)
+                        tc_commit(b_empty(bs));
+                }
+                __syncwarp();
             }
-            g0 += static_cast<uint32_t>(steps);
-            g1 += in_use == 2 ? static_cast<uint32_t>(steps) : 0u;
+            c0 += static_cast<uint32_t>(steps);
+            g0 += static_cast<uint32_t>(steps), ++n_p0;
+            if (in_use == 2)
+                g1 += static_cast<uint32_t>(steps), ++n_p1;
             n += steps;
             walk_next_segment<kChunkTile, kChunkRows>(p, w);
         }
@@ -432,10 +437,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         uint32_t vs = 0, vph = 0, bs = 0, bph = 1;
 #pragma unroll 1
         for (int64_t h = 0; h < count; ++h) {
-            if (!wait(v_full(vs), vph) || !wait(b_empty(bs), bph))
-                break;
+            wait2(v_full(vs), vph, b_empty(bs), bph);
             const uint32_t src = base + C::V_OFF + vs * C::V_STAGE, dst = base + C::B_OFF + bs * C::B_STAGE;
-#pragma unroll 2
+#pragma unroll 4
             for (uint32_t i = 0; i < D / 16; ++i) {
                 const uint32_t m = (D == 128 ? i >> 1 : i) * 8u + (warp - 2u) * 4u + (lane >> 3);
                 const uint32_t key = (2u * m) ^ ((lane & 4u) ? 5u : 0u), atom = D == 128 ? i & 1u : 0u;
@@ -472,19 +476,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u;
         const uint32_t o_addr = s_addr + 256u;
         const uint32_t prow = base + C::P_OFF + tile * 2u * C::P_BUF + static_cast<uint32_t>(r) * 128u;
-        uint32_t g = 0;        // steps of this tile
+        uint32_t g = 0, it = 0;   // steps, and iterations (two more a piece), of this tile
         bool open = false;
         int64_t n = 0;
         while (n < count) {
             const int32_t steps = piece_steps(n), rows = piece_rows(), r0 = w.q * kChunkRows;
             const uint32_t n0 = static_cast<uint32_t>(n);
-            if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile: its part in freeing the scales
-                if (lane == 0)
-                    for (int32_t k = 0; k < steps; ++k) {
-                        ok = ok && mbar_wait_tries(sc_empty((n0 + k) % NS), (((n0 + k) / NS) & 1u) ^ 1u, abort);
-                        mbar_arrive(sc_empty((n0 + k) % NS));
-                    }
-                __syncwarp();
+            if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile
                 n += steps;
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             auto look = [&](int32_t k) {
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
-                const uint32_t there = meta[(n0 + k) % NS];
+                const uint32_t there = meta[(n0 + k) % NK];
                 if (j0 + 63 <= pos_first && (j0 >= low_last || j0 + 64 <= p.sinks) && there == all_boxes)
                     return true;
 #pragma unroll
@@ -597,7 +595,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // The loop handles a step's exponentials together with the scaling of the next one's
             // logits, column by column in the same registers: the two use different pipes.
             uint32_t acc[32];
-            wait_lane(s_full(tile, g & 1u), (g >> 1) & 1u);
+            wait(done(tile, it & 1u), (it >> 1) & 1u);
+            ++it;
             tc_fence_after_sync();
             bool whole = look(0);
 #pragma unroll
@@ -606,18 +605,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NS) * 512u + (h * 32 + e) * 4);
+                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NK) * 512u + (h * 32 + e) * 4);
             }
             if (!whole)
                 hide();
 #pragma unroll 1
-            for (int32_t k = 0; k < steps; ++k, ++g) {
-                const uint32_t b = g & 1u, ph = (g >> 1) & 1u, ss = (n0 + k) % NS;
-                const uint32_t svb = base + C::SC_OFF + ss * 512u + 256u;
-                const uint32_t skb = base + C::SC_OFF + ((n0 + k + 1) % NS) * 512u;
+            for (int32_t k = 0; k < steps; ++k, ++g, ++it) {
+                const uint32_t b = g & 1u;
+                const uint32_t svb = base + C::SC_OFF + ((n0 + k) % NK) * 512u + 256u;
+                const uint32_t skb = base + C::SC_OFF + ((n0 + k + 1) % NK) * 512u;
                 const bool more = k + 1 < steps;
+                // S of step k + 1 is there, P(k - 1) V(k - 1) is done: O is stable, and this step's
+                // P buffer has been free since iteration k
+                wait(done(tile, b ^ 1u), (it >> 1) & 1u);
+                tc_fence_after_sync();
                 // the sums are rescaled only when the maximum grows by more than 8 (weights stay
-                // below 2^8 s_v); O is stable once the product of the step before is done
+                // below 2^8 s_v)
                 const float mb = top();
                 const bool grow = mb > m_used + 8.0f;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -625,8 +628,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
                     if (k > 0) {
-                        wait_lane(pv_done(tile, b ^ 1u), ((g - 1u) >> 1) & 1u);
-                        tc_fence_after_sync();
 #pragma unroll 1
                         for (int32_t c = 0; c < D; c += 32) {
                             tmem_ld_32x32b_x32(o_addr + c, acc);
@@ -639,11 +640,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         tmem_st_wait();
                     }
                 }
-                // the P buffer is free once the product of two steps before is done
-                wait_lane(pv_done(tile, b), ph ^ 1u);
-                if (more)
-                    wait_lane(s_full(tile, b ^ 1u), ((g + 1u) >> 1) & 1u);
-                tc_fence_after_sync();
                 const bool was_whole = whole;
                 const uint32_t saw[2] = {see[0], see[1]};
                 if (more)
@@ -690,15 +686,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0)
                     mbar_arrive(p_full(tile, b));
-                    mbar_arrive(sc_empty(ss));
-                }
                 if (more && !whole)
                     hide();
             }
             const bool begins = w.i == 0, ends = w.i + steps == w.t.nt, finish = begins && ends;
-            wait_lane(pv_done(tile, (g - 1u) & 1u), ((g - 1u) >> 1) & 1u);
+            wait(done(tile, it & 1u), (it >> 1) & 1u);
+            ++it;
             tc_fence_after_sync();
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
