@@ -6,12 +6,13 @@
 // - warp 0 streams keys, values and scales page by page through TMA rings;
 // - warps 2 and 3 turn each step's value codes into bf16 (times 2^-6, exact), the
 //   128-byte-swizzled operand of the second product;
-// - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) two steps ahead of
+// - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) three steps ahead of
 //   O_t += P_t V (kind::f16, fp32 in TMEM): logits and P of a tile have two buffers each, so
 //   that its softmax never waits for a product just issued. A commit costs the issuing warp
 //   about 200 cycles and a wait 110 or more, so there is one commit a tile and step: `done` of
-//   iteration k covers S(k) and P(k - 2) V(k - 2), and everything else follows from the
-//   softmax's "P written": K(k) and its scales may be replaced, P(k - 1) V(k - 1) is done;
+//   iteration k covers S(k) and P(k - 3) V(k - 3), and the rest follows from the softmax's
+//   "P(k - 3) written": S(k - 2) is done with K(k - 2) and has been read, the scales of step
+//   k - 3 have been read, P(k - 5) V(k - 5) is done;
 // - warps 4..7 (tile 0) and 8..11 (tile 1), one thread a query row, rotate and quantize their
 //   query rows into the operand tile, then per step form 64 base-2 logits, an online softmax
 //   (sums rescaled only when the maximum grows by more than 8), and P = probability * s_v in
@@ -30,7 +31,7 @@ constexpr int kChunkThreads = 384;
 
 template <int D>
 struct ChunkConfig {
-    static constexpr int NK = 4, NV = 3, NB = 4;   // stages: K and scales, value codes, bf16 values
+    static constexpr int NK = 4, NV = 3, NB = 4, NS = 8;   // stages: K, value codes, bf16 values, scales
     static constexpr int Q_TILE = 128 * D, K_STAGE = 64 * D, V_STAGE = 64 * D, B_STAGE = 64 * D * 2;
     static constexpr int P_BUF = 128 * 64 * 2;
     static constexpr int Q_OFF = 0;
@@ -39,14 +40,16 @@ struct ChunkConfig {
     static constexpr int B_OFF = K_OFF + NK * K_STAGE;
     static constexpr int V_OFF = B_OFF + NB * B_STAGE;
     static constexpr int SC_OFF = V_OFF + NV * V_STAGE;     // 64 key scales, 64 value scales a stage
-    static constexpr int QS_OFF = SC_OFF + NK * 512;        // query scales
+    static constexpr int QS_OFF = SC_OFF + NS * 512;        // query scales
     static constexpr int BAR_OFF = QS_OFF + kChunkRows * 4;
     // full and empty of each ring, then per tile and buffer done and p_full; q_full; drain
     static constexpr int NBARS = 2 * (NK + NV + NB) + 8 + 2 + 1;
-    static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each K stage
-    static constexpr int HOLD_OFF = META_OFF + NK * 4;      // TMEM address, abort flag, scan result
+    static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
+    static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
     static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
     static_assert((NK & (NK - 1)) == 0 && (NB & (NB - 1)) == 0, "ring positions are masked");
+    // step h is loaded once P(h - NK - 1) is written, so that step h - NS - 1 and older are read
+    static_assert(NS >= NK + 2 && (NS & (NS - 1)) == 0, "the scales need no barriers of their own");
     static constexpr int64_t PIECE = static_cast<int64_t>(kChunkRows) * (D + 2);   // floats, as FewConfig's
     static_assert(SMEM_BYTES + 256 <= 232448, "shared memory per block");
 };
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ CUtensorMap tmPool, const PagedParams p)
 {
     using C = ChunkConfig<D>;
-    constexpr int NK = C::NK, NV = C::NV, NB = C::NB;
+    constexpr int NK = C::NK, NV = C::NV, NB = C::NB, NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        uint32_t ks = 0, kph = 1, vs = 0, vph = 1;
+        uint32_t ks = 0, kph = 1, vs = 0, vph = 1, ss = 0;
         int64_t n = 0, issued = 0;
         while (ok && n < count) {
             const int32_t steps = piece_steps(n);
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 if (!ok)
                     break;
                 if (lane == 0) {
-                    meta[ks] = valid;
+                    meta[ss] = valid;
                     mbar_arrive_expect_tx(k_full(ks), keys * (D + 8u));
                     mbar_arrive_expect_tx(v_full(vs), keys * D);
                 }
@@ -336,11 +339,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 ++issued;
                 if (mine) {
                     tma_load_2d(base + C::K_OFF + ks * C::K_STAGE + lane * pp * D, &tmPool, k_full(ks), 0, krow);
-                    const uint32_t sdst = base + C::SC_OFF + ks * 512u + lane * pp * 4u;
+                    const uint32_t sdst = base + C::SC_OFF + ss * 512u + lane * pp * 4u;
                     bulk_load_1d(sdst, p.scales + krow, 4u * pp, k_full(ks));
                     bulk_load_1d(sdst + 256u, p.scales + vrow, 4u * pp, k_full(ks));
                     tma_load_2d(base + C::V_OFF + vs * C::V_STAGE + lane * pp * D, &tmPool, v_full(vs), 0, vrow);
                 }
+                ss = (ss + 1u) % NS;
                 if (++ks == NK)
                     ks = 0, kph ^= 1u;
                 if (++vs == NV)
@@ -367,62 +371,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // operand descriptors; 16 bytes further on is 1 more
         const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
         const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
-        // steps of all pieces so far; steps of each tile's pieces, and these pieces
-        uint32_t c0 = 0, g0 = 0, g1 = 0, n_p0 = 0, n_p1 = 0;
+        // steps of all pieces so far, and of each tile's pieces
+        uint32_t c0 = 0, g0 = 0, g1 = 0;
         int64_t n = 0;
         while (n < count) {
             const int32_t steps = piece_steps(n);
             const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
-            // iteration k: S of step k goes out when P of step k - 2 is written (that S buffer has
+            // iteration k: S(k) goes out when P(k - 3) is written (S(k - 2), its buffer's last, has
             // been read then), just before the product of that P with V
 #pragma unroll 1
-            for (int32_t k = 0; k < steps + 2; ++k) {
-                const uint32_t c = c0 + static_cast<uint32_t>(k), ks = c % NK, bs = (c - 2u) % NB;   // ring positions
-                if (k >= 2 && k < steps)
-                    wait2(k_full(ks), (c / NK) & 1u, b_full(bs), ((c - 2u) / NB) & 1u);
-                else if (k < steps)
+            for (int32_t k = 0; k < steps + 3; ++k) {
+                const uint32_t c = c0 + static_cast<uint32_t>(k), ks = c % NK, bs = (c - 3u) % NB;   // ring positions
+                const bool s_now = k < steps, pv_now = k >= 3;
+                if (s_now && pv_now)
+                    wait2(k_full(ks), (c / NK) & 1u, b_full(bs), ((c - 3u) / NB) & 1u);
+                else if (s_now)
                     wait(k_full(ks), (c / NK) & 1u);
-                else if (k >= 2)
-                    wait(b_full(bs), ((c - 2u) / NB) & 1u);
+                else if (pv_now)
+                    wait(b_full(bs), ((c - 3u) / NB) & 1u);
 #pragma unroll 1
                 for (uint32_t t = 0; t < in_use; ++t) {
                     const uint32_t g = (t == 0 ? g0 : g1) + static_cast<uint32_t>(k), b = g & 1u;
-                    if (k >= 2)
-                        wait(p_full(t, b), ((g >> 1) & 1u) ^ 1u);
-                    else if (k == 0)
-                        wait(q_full(t), (t == 0 ? n_p0 : n_p1) & 1u);
+                    if (pv_now)
+                        wait(p_full(t, b ^ 1u), ((g - 3u) >> 1) & 1u);
+                    else if (k == 0 || k == 2)   // Q is there; S(0) has been read
+                        wait(q_full(t), static_cast<uint32_t>(k) >> 1);
                     tc_fence_after_sync();
                     const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
-                    const uint64_t pa = dp + (2 * t + b) * (C::P_BUF >> 4), va = db + bs * (C::B_STAGE >> 4);
+                    const uint64_t pa = dp + (2 * t + (b ^ 1u)) * (C::P_BUF >> 4), va = db + bs * (C::B_STAGE >> 4);
                     if (leader) {
-                        if (k < steps) {
+                        if (s_now) {
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
                                 mma_s8(tmem_base + t * 128 + b * 64, qa + 2 * kk, ka + 2 * kk, IDESC_S, kk != 0 ? 1u : 0u);
                         }
-                        if (k >= 2) {
+                        if (pv_now) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, k > 2 || kk != 0 ? 1u : 0u);
+                                mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, k > 3 || kk != 0 ? 1u : 0u);
                         }
                         tc_commit(done(t, b));
                     }
                     __syncwarp();
                 }
-                if (leader) {
-                    if (k >= 2)       // every P of step k - 2 is written: its K and scales are read
+                if (leader && pv_now) {
+                    if (k == 3)
+                        mbar_arrive(k_empty((c - 3u) % NK));
+                    if (k < steps + 2)
                         mbar_arrive(k_empty((c - 2u) % NK));
-                    if (k >= 3)       // and its writers saw the product of step k - 3 done
-                        mbar_arrive(b_empty((c - 3u) % NB));
-                    if (k == steps + 1)
+                    if (k >= 5)
+                        mbar_arrive(b_empty((c - 5u) % NB));
+                    if (k == steps + 2) {
+                        if (steps > 1)
+                            tc_commit(b_empty((c - 4u) % NB));
                         tc_commit(b_empty(bs));
+                    }
                 }
                 __syncwarp();
             }
             c0 += static_cast<uint32_t>(steps);
-            g0 += static_cast<uint32_t>(steps), ++n_p0;
-            if (in_use == 2)
-                g1 += static_cast<uint32_t>(steps), ++n_p1;
+            g0 += static_cast<uint32_t>(steps);
+            g1 += in_use == 2 ? static_cast<uint32_t>(steps) : 0u;
             n += steps;
             walk_next_segment<kChunkTile, kChunkRows>(p, w);
         }
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u;
         const uint32_t o_addr = s_addr + 256u;
         const uint32_t prow = base + C::P_OFF + tile * 2u * C::P_BUF + static_cast<uint32_t>(r) * 128u;
-        uint32_t g = 0, it = 0;   // steps, and iterations (two more a piece), of this tile
+        uint32_t g = 0, parity = 0;   // steps of this tile; bit b: parity of the next phase of done(tile, b)
         bool open = false;
         int64_t n = 0;
         while (n < count) {
@@ -550,7 +559,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             auto look = [&](int32_t k) {
                 const int32_t i = w.i + k;
                 const int32_t j0 = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile;
-                const uint32_t there = meta[(n0 + k) % NK];
+                const uint32_t there = meta[(n0 + k) % NS];
                 if (j0 + 63 <= pos_first && (j0 >= low_last || j0 + 64 <= p.sinks) && there == all_boxes)
                     return true;
 #pragma unroll
@@ -595,8 +604,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // The loop handles a step's exponentials together with the scaling of the next one's
             // logits, column by column in the same registers: the two use different pipes.
             uint32_t acc[32];
-            wait(done(tile, it & 1u), (it >> 1) & 1u);
-            ++it;
+            auto next_done = [&](uint32_t b) {   // (none may be left out: a wait sees only the parity)
+                wait(done(tile, b), (parity >> b) & 1u);
+                parity ^= 1u << b;
+            };
+            next_done(g & 1u);
             tc_fence_after_sync();
             bool whole = look(0);
 #pragma unroll
@@ -605,19 +617,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
-                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NK) * 512u + (h * 32 + e) * 4);
+                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NS) * 512u + (h * 32 + e) * 4);
             }
             if (!whole)
                 hide();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full(tile));   // (its second phase of the piece: S(0) has been read)
 #pragma unroll 1
-            for (int32_t k = 0; k < steps; ++k, ++g, ++it) {
+            for (int32_t k = 0; k < steps; ++k, ++g) {
                 const uint32_t b = g & 1u;
-                const uint32_t svb = base + C::SC_OFF + ((n0 + k) % NK) * 512u + 256u;
-                const uint32_t skb = base + C::SC_OFF + ((n0 + k + 1) % NK) * 512u;
+                const uint32_t svb = base + C::SC_OFF + ((n0 + k) % NS) * 512u + 256u;
+                const uint32_t skb = base + C::SC_OFF + ((n0 + k + 1) % NS) * 512u;
                 const bool more = k + 1 < steps;
-                // S of step k + 1 is there, P(k - 1) V(k - 1) is done: O is stable, and this step's
-                // P buffer has been free since iteration k
-                wait(done(tile, b ^ 1u), (it >> 1) & 1u);
+                // S(k + 1) is there, and P(k - 2) V(k - 2) is done: this step's P buffer is free
+                next_done(b ^ 1u);
                 tc_fence_after_sync();
                 // the sums are rescaled only when the maximum grows by more than 8 (weights stay
                 // below 2^8 s_v)
@@ -627,7 +642,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     const float alpha = grow ? ex2_approx(m_used - mb) : 1.0f;
                     m_used = grow ? mb : m_used;
                     l_sum *= alpha;
-                    if (k > 0) {
+                    if (k > 0) {   // O is stable once P(k - 1) V(k - 1) is done
+                        wait(done(tile, b), (parity >> b) & 1u);
+                        tc_fence_after_sync();
 #pragma unroll 1
                         for (int32_t c = 0; c < D; c += 32) {
                             tmem_ld_32x32b_x32(o_addr + c, acc);
@@ -692,8 +709,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     hide();
             }
             const bool begins = w.i == 0, ends = w.i + steps == w.t.nt, finish = begins && ends;
-            wait(done(tile, it & 1u), (it >> 1) & 1u);
-            ++it;
+            next_done((g + 1u) & 1u);
+            next_done(g & 1u);
             tc_fence_after_sync();
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
