@@ -12,6 +12,7 @@
 
 #include "attention.cuh"
 #include "device.cuh"
+#include "kvcache.cuh"
 #include "rotquant.cuh"
 
 namespace sdnq {
@@ -368,15 +369,6 @@ struct FewDesc {       // the segment that begins in a block and goes on behind 
     int32_t head0;     // first head of the share
     int32_t r0;        // first (token, head) row of the tile
 };
-
-__device__ __forceinline__ void mma_m16n8k32_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1,
-                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
-                 " {%8, %9}, {%0, %1, %2, %3};"
-                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ void mma_m16n8k16_bf16(float (&d)[4], uint32_t a0, uint32_t a1,
                                                   uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)

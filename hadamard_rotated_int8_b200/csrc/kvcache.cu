@@ -55,17 +55,22 @@ sdnq_status validate_kv_rows(const void *k, int64_t ldk, const void *v, int64_t 
     return SDNQ_OK;
 }
 
-template <bool WRITE, int G, int D>
-void launch_kv(const KvParams &p, int sm_count, cudaStream_t cs)
+// Persistent grids: the blocks that the SMs hold at once.
+template <int G, int D>
+void launch_kv_write(const KvParams &p, int sm_count, cudaStream_t cs)
 {
-    constexpr int rows_per_warp = 1024 / D;
-    const int64_t chunks = (p.rows + rows_per_warp - 1) / rows_per_warp;
-    int64_t blocks = (chunks + 7) / 8;
-    const int64_t most = static_cast<int64_t>(sm_count) * 8;
-    if (blocks > most)
-        blocks = most;
-    launch_programmatic(WRITE ? kv_write_kernel<G, D> : kv_read_kernel<G, D>,
-                        dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, p);
+    const int64_t blocks = (p.rows + 8 * (1024 / D) - 1) / (8 * (1024 / D)), most = static_cast<int64_t>(sm_count) * 4;
+    launch_programmatic(kv_write_kernel<G, D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0,
+                        cs, p);
+}
+
+template <int D>
+void launch_kv_read(const KvParams &p, int sm_count, cudaStream_t cs)
+{
+    constexpr int rows = 16 * (kReadThreads / 32);
+    const int64_t blocks = (p.rows + rows - 1) / rows, most = static_cast<int64_t>(sm_count) * 4;
+    launch_programmatic(kv_read_kernel<D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kReadThreads), 0,
+                        cs, p);
 }
 
 template <bool WRITE>
@@ -95,23 +100,26 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     p.nslots = pages * page;
     p.Hkv = static_cast<int32_t>(Hkv);
     p.page_shift = log2_of(page);
+    p.group = static_cast<int32_t>(g);
     p.c_g = rotation_factor(g);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
-    if (D == 128) {
+    if (!WRITE) {
+        D == 128 ? launch_kv_read<128>(p, dev.sm_count, cs) : launch_kv_read<64>(p, dev.sm_count, cs);
+    } else if (D == 128) {
         switch (g) {
-        case 8: launch_kv<WRITE, 8, 128>(p, dev.sm_count, cs); break;
-        case 16: launch_kv<WRITE, 16, 128>(p, dev.sm_count, cs); break;
-        case 32: launch_kv<WRITE, 32, 128>(p, dev.sm_count, cs); break;
-        case 64: launch_kv<WRITE, 64, 128>(p, dev.sm_count, cs); break;
-        default: launch_kv<WRITE, 128, 128>(p, dev.sm_count, cs); break;
+        case 8: launch_kv_write<8, 128>(p, dev.sm_count, cs); break;
+        case 16: launch_kv_write<16, 128>(p, dev.sm_count, cs); break;
+        case 32: launch_kv_write<32, 128>(p, dev.sm_count, cs); break;
+        case 64: launch_kv_write<64, 128>(p, dev.sm_count, cs); break;
+        default: launch_kv_write<128, 128>(p, dev.sm_count, cs); break;
         }
     } else {
         switch (g) {
-        case 8: launch_kv<WRITE, 8, 64>(p, dev.sm_count, cs); break;
-        case 16: launch_kv<WRITE, 16, 64>(p, dev.sm_count, cs); break;
-        case 32: launch_kv<WRITE, 32, 64>(p, dev.sm_count, cs); break;
-        default: launch_kv<WRITE, 64, 64>(p, dev.sm_count, cs); break;
+        case 8: launch_kv_write<8, 64>(p, dev.sm_count, cs); break;
+        case 16: launch_kv_write<16, 64>(p, dev.sm_count, cs); break;
+        case 32: launch_kv_write<32, 64>(p, dev.sm_count, cs); break;
+        default: launch_kv_write<64, 64>(p, dev.sm_count, cs); break;
         }
     }
     return launch_status();

@@ -12,8 +12,8 @@
 // read:  x = bf16(butterfly(code) * fp32(s * c)); the butterfly of whole numbers is exact in
 //        fp32 (|sum| <= 128 * 128).
 //
-// Both are bound by memory: 2 D bytes of bf16 and D + 4 bytes of codes and scale per row. One
-// warp takes 1024 elements = 1024 / D consecutive (token, key-or-value, head) rows at a time
+// Both are bound by memory: 2 D bytes of bf16 and D + 4 bytes of codes and scale per row. In
+// the writer one warp takes 1024 elements = 1024 / D consecutive (token, key-or-value, head) rows at a time
 // with the lane mapping of the rotate+quantize kernel (four 16-byte vectors a lane in flight,
 // fully used 128-byte lines); a row's maximum combines its 8 lanes by shuffles.
 #pragma once
@@ -33,35 +33,51 @@ struct KvParams {
     int64_t nslots;         // pages * page
     int32_t Hkv;
     int32_t page_shift;     // log2(page)
+    int32_t group;          // min(group, D)
     float c_g;
 };
 
-// Where row r = (t * 2 + which) * Hkv + h lives: the bf16 row and the cache row (-1: none).
-__device__ __forceinline__ void kv_locate(const KvParams &p, int64_t r, int32_t D,
-                                          uint16_t *&x, int64_t &cache_row)
+// Row r = (t * 2 + which) * Hkv + h of the call.
+struct KvRow {
+    int64_t t;
+    uint32_t h;
+    bool is_v;
+};
+
+__device__ __forceinline__ KvRow kv_row(const KvParams &p, int64_t r)
 {
     const uint32_t H2 = 2u * static_cast<uint32_t>(p.Hkv);
-    int64_t t;
+    KvRow k;
     uint32_t rem;
     if (r < (1ll << 31)) {   // 64-bit division is slow; nearly every call stays below
-        t = static_cast<uint32_t>(r) / H2;
-        rem = static_cast<uint32_t>(r) - static_cast<uint32_t>(t) * H2;
+        k.t = static_cast<uint32_t>(r) / H2;
+        rem = static_cast<uint32_t>(r) - static_cast<uint32_t>(k.t) * H2;
     } else {
-        t = r / H2;
-        rem = static_cast<uint32_t>(r - t * H2);
+        k.t = r / H2;
+        rem = static_cast<uint32_t>(r - k.t * H2);
     }
-    const bool is_v = rem >= static_cast<uint32_t>(p.Hkv);
-    const uint32_t h = is_v ? rem - static_cast<uint32_t>(p.Hkv) : rem;
-    x = (is_v ? p.v + t * p.ldv : p.k + t * p.ldk) + static_cast<int64_t>(h) * D;
-    const int64_t slot = p.slots[t];
-    cache_row = -1;
+    k.is_v = rem >= static_cast<uint32_t>(p.Hkv);
+    k.h = k.is_v ? rem - static_cast<uint32_t>(p.Hkv) : rem;
+    return k;
+}
+
+// Its bf16 row.
+__device__ __forceinline__ uint16_t *kv_plain(const KvParams &p, const KvRow &k, int32_t D)
+{
+    return (k.is_v ? p.v + k.t * p.ldv : p.k + k.t * p.ldk) + static_cast<int64_t>(k.h) * D;
+}
+
+// Its row in the cache (-1: none).
+__device__ __forceinline__ int64_t kv_held(const KvParams &p, const KvRow &k, int64_t slot)
+{
     if (slot >= 0 && slot < p.nslots) {
         const int64_t id = slot >> p.page_shift;
         const int64_t off = slot & ((1ll << p.page_shift) - 1);
-        cache_row = (((id * p.Hkv + h) * 2 + (is_v ? 1 : 0)) << p.page_shift) + off;
-    } else if (slot >= 0) {
-        atomicOr(&g_device_error, kDevIndex);
+        return (((id * p.Hkv + k.h) * 2 + (k.is_v ? 1 : 0)) << p.page_shift) + off;
     }
+    if (slot >= 0)
+        atomicOr(&g_device_error, kDevIndex);
+    return -1;
 }
 
 template <int G, int D>
@@ -82,10 +98,13 @@ __global__ void __launch_bounds__(256, 4) kv_write_kernel(const KvParams p)
         uint4 raw[4];
 #pragma unroll
         for (int r = 0; r < RPL; ++r) {
-            uint16_t *x = nullptr;
+            const uint16_t *x = nullptr;
             crow[r] = -1;
-            if (row0 + r < p.rows)
-                kv_locate(p, row0 + r, D, x, crow[r]);
+            if (row0 + r < p.rows) {
+                const KvRow k = kv_row(p, row0 + r);
+                x = kv_plain(p, k, D);
+                crow[r] = kv_held(p, k, p.slots[k.t]);
+            }
 #pragma unroll
             for (int u = 0; u < VPR; ++u)
                 raw[r * VPR + u] = crow[r] >= 0 ? ld_nc_v4(x + u * 64 + (lane & 7u) * 8)
@@ -126,61 +145,158 @@ __global__ void __launch_bounds__(256, 4) kv_write_kernel(const KvParams p)
     }
 }
 
-template <int G, int D>
-__global__ void __launch_bounds__(256, 4) kv_read_kernel(const KvParams p)
+// d += a * b^T, a 16 rows of 32 int8, b 8 rows of 32 int8, int32 sums.
+__device__ __forceinline__ void mma_m16n8k32_s8(int32_t (&d)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    constexpr int RPL = 256 / D, VPR = 4 / RPL;
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+                 " {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 or 4 bytes global -> shared without registers, zeros instead where `from` is null;
+// completion by groups of this thread.
+__device__ __forceinline__ void async_copy_16(uint32_t to, const void *from, const void *any)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from ? from : any), "r"(from ? 16u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void async_copy_4(uint32_t to, const void *from, const void *any)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from ? from : any), "r"(from ? 4u : 0u)
+                 : "memory");
+}
+
+// The reader's butterfly is a product of whole numbers, exact in any order, so its five inner
+// stages are int8 matrix instructions: a warp takes 16 rows, lane (q, t) has elements
+// [8 t, 8 t + 8) of each 32 of rows q and q + 8, and the 32 x 32 block of signs (zeros between
+// groups below 32) sits in 8 registers with its rows and columns in the order that gives the
+// lane the same elements of the result. The stages at distance 32 and 64 add what the lane has.
+// About 300 instructions for 2048 elements (in fp32 with shuffles: 900). What bounds it is the
+// number of rows on their way, 128 bytes each from anywhere: every warp keeps kReadStages - 1
+// tiles of 16 in flight through its own ring in shared memory.
+constexpr int kReadThreads = 128, kReadStages = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvParams p)
+{
+    constexpr int NG = D / 32, CH = D / 16, ST = kReadStages;
+    // a stage: 16 rows at 128 bytes, 16-byte chunk c of row r at c ^ (r & 7); then 16 scales
+    constexpr uint32_t STAGE = 16 * 128 + 64;
+    __shared__ __align__(128) uint8_t ring[kReadThreads / 32][ST][STAGE];
     grid_dependents_launch();
     grid_dependency_wait();
-    const uint32_t lane = lane_id();
-    const int64_t nchunks = (p.rows + 4 * RPL - 1) / (4 * RPL);
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    for (int64_t c = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-         c < nchunks; c += warps) {
-        const int64_t row0 = c * (4 * RPL) + static_cast<int64_t>(lane >> 3) * RPL;
-        uint16_t *x[RPL];
-        float s[RPL];
-        uint2 raw[4];
+    const uint32_t lane = lane_id(), q = lane >> 2, t = lane & 3u;
+    const uint32_t mine = smem_u32(ring[threadIdx.x >> 5]);
+    uint32_t sign[4][2];
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            int64_t crow = -1;
-            x[r] = nullptr;
-            if (row0 + r < p.rows)
-                kv_locate(p, row0 + r, D, x[r], crow);
-            s[r] = 0.0f;   // no slot: zeros
-            if (crow >= 0)
-                s[r] = p.scales[crow];
+    for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-            for (int u = 0; u < VPR; ++u) {
-                raw[r * VPR + u] = make_uint2(0u, 0u);
-                if (crow >= 0)
-                    raw[r * VPR + u] = *reinterpret_cast<const uint2 *>(
-                        p.codes + crow * D + u * 64 + (lane & 7u) * 8);
+        for (int u = 0; u < 2; ++u) {
+            sign[nb][u] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t k = 8u * t + 4u * u + i, n = 8u * (q >> 1) + 2u * nb + (q & 1u);
+                const uint32_t in_group = static_cast<uint32_t>(p.group - 1);
+                const bool in = ((k ^ n) & ~in_group) == 0u;
+                const uint32_t v = !in ? 0u : (__popc(k & n & in_group) & 1) ? 0xffu : 1u;
+                sign[nb][u] |= v << (8 * i);
             }
         }
-        float v[4][8];
+    const int64_t ntiles = (p.rows + 15) / 16;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kReadThreads / 32);
+    int64_t tile = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
+    // slot of row (lane & 15) of the next tile to be fetched
+    auto slot_of = [&](int64_t tl) {
+        const int64_t row = tl * 16 + (lane & 15u);
+        return row < p.rows ? p.slots[kv_row(p, row).t] : -1ll;
+    };
+    int64_t fetch_tile = tile, slot = slot_of(tile);
+    uint32_t fetch_stage = 0;
+    auto fetch = [&] {
+        const int64_t row = fetch_tile * 16 + (lane & 15u);
+        const int64_t crow = row < p.rows ? kv_held(p, kv_row(p, row), slot) : -1;
+        const uint32_t at = mine + fetch_stage * STAGE;
+        if (fetch_tile < ntiles) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w = i < 4 ? raw[t].x : raw[t].y;
-                v[t][i] = static_cast<float>(static_cast<int8_t>(w >> (8 * (i & 3))));
+            for (int j = 0; j < CH / 2; ++j) {
+                const uint32_t r = (lane / CH) + j * (32 / CH), c = lane % CH;
+                const int64_t from = __shfl_sync(0xffffffffu, crow, static_cast<int>(r));
+                async_copy_16(at + r * 128u + ((c ^ (r & 7u)) << 4), from >= 0 ? p.codes + from * D + c * 16 : nullptr, p.codes);
             }
-        chunk_butterfly<G>(v, lane);
+            if (lane < 16)
+                async_copy_4(at + 2048u + lane * 4u, crow >= 0 ? p.scales + crow : nullptr, p.scales);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        fetch_tile += warps;
+        fetch_stage = (fetch_stage + 1u) % ST;
+        slot = slot_of(fetch_tile);
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i)
+        fetch();
+    uint32_t stage = 0;
+#pragma unroll 1
+    for (; tile < ntiles; tile += warps) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+        __syncwarp();
+        const uint32_t at = mine + stage * STAGE;
+        stage = (stage + 1u) % ST;
+        uint16_t *x[2];
+        float s[2];
+        uint2 raw[2][NG];
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
+        for (int r = 0; r < 2; ++r) {
+            const int64_t row = tile * 16 + q + 8 * r;
+            x[r] = row < p.rows ? kv_plain(p, kv_row(p, row), D) + t * 8 : nullptr;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[r]) : "r"(at + 2048u + (q + 8u * r) * 4u) : "memory");
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(raw[r][i].x), "=r"(raw[r][i].y)
+                             : "r"(at + (q + 8u * r) * 128u + (((2u * i + (t >> 1)) ^ q) << 4) + (t & 1u) * 8u)
+                             : "memory");
+        }
+        __syncwarp();      // the stage that is fetched next has been read by every lane
+        fetch();
+        float v[2][NG][8];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                int32_t d[4] = {0, 0, 0, 0};
+                mma_m16n8k32_s8(d, raw[0][i].x, raw[1][i].x, raw[0][i].y, raw[1][i].y, sign[nb][0], sign[nb][1]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[c >> 1][i][2 * nb + (c & 1)] = static_cast<float>(d[c]);
+            }
+#pragma unroll
+        for (int h = 1; h < NG; h <<= 1)
+            if (p.group > 32 * h) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+                        if ((i & h) == 0) {
+#pragma unroll
+                            for (int c = 0; c < 8; c += 2)
+                                bfly2(v[r][i][c], v[r][i][c + 1], v[r][i + h][c], v[r][i + h][c + 1]);
+                        }
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
             const float f = __fmul_rn(s[r], p.c_g);
-            if (row0 + r < p.rows) {
+            if (x[r] != nullptr) {
 #pragma unroll
-                for (int u = 0; u < VPR; ++u) {
+                for (int i = 0; i < NG; ++i) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h2 =
-                            __floats2bfloat162_rn(v[r * VPR + u][2 * i] * f, v[r * VPR + u][2 * i + 1] * f);
-                        w[i] = *reinterpret_cast<const uint32_t *>(&h2);
+                    for (int c = 0; c < 4; ++c) {
+                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[r][i][2 * c] * f, v[r][i][2 * c + 1] * f);
+                        w[c] = *reinterpret_cast<const uint32_t *>(&h2);
                     }
-                    st_v4(x[r] + u * 64 + (lane & 7u) * 8, w[0], w[1], w[2], w[3]);
+                    st_v4(x[r] + i * 32, w[0], w[1], w[2], w[3]);
                 }
             }
         }
