@@ -67,8 +67,8 @@ void launch_kv_write(const KvParams &p, int sm_count, cudaStream_t cs)
 template <int D>
 void launch_kv_read(const KvParams &p, int sm_count, cudaStream_t cs)
 {
-    constexpr int rows = 16 * (kReadThreads / 32);
-    const int64_t blocks = (p.rows + rows - 1) / rows, most = static_cast<int64_t>(sm_count) * 4;
+    constexpr int warps = kReadThreads / 32;
+    const int64_t blocks = ((p.T + 15) / 16 * (2 * p.Hkv) + warps - 1) / warps, most = static_cast<int64_t>(sm_count) * 4;
     launch_programmatic(kv_read_kernel<D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kReadThreads), 0,
                         cs, p);
 }
@@ -96,6 +96,7 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     p.slots = slots;
     p.codes = codes;
     p.scales = scales;
+    p.T = T;
     p.rows = T * 2 * Hkv;
     p.nslots = pages * page;
     p.Hkv = static_cast<int32_t>(Hkv);

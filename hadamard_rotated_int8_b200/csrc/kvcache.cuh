@@ -29,7 +29,7 @@ struct KvParams {
     const int64_t *slots;   // [T]; negative: the token has no slot
     int8_t *codes;
     float *scales;
-    int64_t rows;           // T * 2 * Hkv
+    int64_t T, rows;        // rows = T * 2 * Hkv
     int64_t nslots;         // pages * page
     int32_t Hkv;
     int32_t page_shift;     // log2(page)
@@ -169,7 +169,7 @@ __device__ __forceinline__ void async_copy_4(uint32_t to, const void *from, cons
 }
 
 // The reader's butterfly is a product of whole numbers, exact in any order, so its five inner
-// stages are int8 matrix instructions: a warp takes 16 rows, lane (q, t) has elements
+// stages are int8 matrix instructions: a warp takes 16 tokens of a head, lane (q, t) has elements
 // [8 t, 8 t + 8) of each 32 of rows q and q + 8, and the 32 x 32 block of signs (zeros between
 // groups below 32) sits in 8 registers with its rows and columns in the order that gives the
 // lane the same elements of the result. The stages at distance 32 and 64 add what the lane has.
@@ -179,7 +179,7 @@ __device__ __forceinline__ void async_copy_4(uint32_t to, const void *from, cons
 constexpr int kReadThreads = 128, kReadStages = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvParams p)
+__global__ void __launch_bounds__(kReadThreads, 4) kv_read_kernel(const KvParams p)
 {
     constexpr int NG = D / 32, CH = D / 16, ST = kReadStages;
     // a stage: 16 rows at 128 bytes, 16-byte chunk c of row r at c ^ (r & 7); then 16 scales
@@ -204,19 +204,19 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvParams p)
                 sign[nb][u] |= v << (8 * i);
             }
         }
-    const int64_t ntiles = (p.rows + 15) / 16;
+    // tile: (16 tokens, key or value, head)
+    const int64_t ntiles = (p.T + 15) / 16 * (2 * p.Hkv);
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kReadThreads / 32);
     int64_t tile = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
-    // slot of row (lane & 15) of the next tile to be fetched
+    // slot of token (lane & 15) of the next tile to be fetched
     auto slot_of = [&](int64_t tl) {
-        const int64_t row = tl * 16 + (lane & 15u);
-        return row < p.rows ? p.slots[kv_row(p, row).t] : -1ll;
+        const int64_t tok = kv_row(p, tl).t * 16 + (lane & 15u);
+        return tok < p.T ? p.slots[tok] : -1ll;
     };
     int64_t fetch_tile = tile, slot = slot_of(tile);
     uint32_t fetch_stage = 0;
     auto fetch = [&] {
-        const int64_t row = fetch_tile * 16 + (lane & 15u);
-        const int64_t crow = row < p.rows ? kv_held(p, kv_row(p, row), slot) : -1;
+        const int64_t crow = kv_held(p, kv_row(p, fetch_tile), slot);
         const uint32_t at = mine + fetch_stage * STAGE;
         if (fetch_tile < ntiles) {
 #pragma unroll
@@ -246,10 +246,11 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvParams p)
         uint16_t *x[2];
         float s[2];
         uint2 raw[2][NG];
+        KvRow k = kv_row(p, tile);
+        k.t = k.t * 16 + q;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t row = tile * 16 + q + 8 * r;
-            x[r] = row < p.rows ? kv_plain(p, kv_row(p, row), D) + t * 8 : nullptr;
+        for (int r = 0; r < 2; ++r, k.t += 8) {
+            x[r] = k.t < p.T ? kv_plain(p, k, D) + t * 8 : nullptr;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[r]) : "r"(at + 2048u + (q + 8u * r) * 4u) : "memory");
 #pragma unroll
             for (int i = 0; i < NG; ++i)
