@@ -91,63 +91,6 @@ __device__ __forceinline__ void thread_butterfly(float (&v)[D], int32_t g)
         }
 }
 
-// Four query rows of D, 8 lanes each with D / 8 consecutive elements: rotated and quantized as
-// the row quantizer does it. Returns the codes, packed, and the row's scale.
-template <int D>
-__device__ __forceinline__ void quant_rows8(float (&v)[D / 8], int32_t g, float c_g, uint32_t lane,
-                                            uint32_t (&codes)[D / 32], float &s)
-{
-    constexpr int E = D / 8;
-#pragma unroll
-    for (int h = 1; h < E; h <<= 1)
-        if (h < 8 || h < g) {
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                if ((i & h) == 0) {
-                    const float a = v[i], b = v[i + h];
-                    v[i] = __fadd_rn(a, b);
-                    v[i + h] = __fsub_rn(a, b);
-                }
-        }
-#pragma unroll
-    for (int x = 1; x < 8; x <<= 1)
-        if (x * E < g) {
-            const float sgn = (lane & x) ? -1.0f : 1.0f;
-#pragma unroll
-            for (int i = 0; i < E; ++i)
-                v[i] = __fmaf_rn(v[i], sgn, __shfl_xor_sync(0xffffffffu, v[i], x));
-        }
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-    for (int x = 1; x < 8; x <<= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float s_z = __fdiv_rn(m, 127.0f);
-    const bool zero = !(m > 0.0f);
-    float s_q = s_z;
-    if (s_z < 0x1p-126f) {   // a subnormal step: the same quotients, 2^64 times as large on both sides
-        s_q = s_z * 0x1p64f;
-        const float most = s_q * 127.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            v[i] = fminf(fmaxf(v[i] * 0x1p64f, -most), most);
-    }
-    const float rcp = __frcp_rn(s_q);
-#pragma unroll
-    for (int c = 0; c < E / 8; ++c) {
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            z[i] = v[8 * c + i];
-        const uint2 w = quant8(z, s_q, rcp, true);
-        codes[2 * c] = zero ? 0u : w.x;
-        codes[2 * c + 1] = zero ? 0u : w.y;
-    }
-    s = zero ? 0.0f : __fmul_rn(s_z, c_g);
-}
-
 // Waits for a phase in a handful of instructions (the loops of this kernel's roles share one
 // instruction cache, and mbar_wait_bounded's clock costs six times the code). Gives up after
 // `kWaitTries` tries (each up to about a microsecond where the hardware suspends the thread):
@@ -535,7 +478,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     uint32_t codes[D / 32];
                     float sq;
-                    quant_rows8<D>(v, p.group, p.c_g, lane, codes, sq);
+                    quant_row_lanes<E, 8>(v, p.group, p.c_g, lane, codes, sq);
                     const uint32_t row = static_cast<uint32_t>(row0 + it * 4), c = lane & 7u;
                     const uint32_t at = base + C::Q_OFF + tile * C::Q_TILE + row * D;
                     if (D == 128)

@@ -56,12 +56,13 @@ sdnq_status validate_kv_rows(const void *k, int64_t ldk, const void *v, int64_t 
 }
 
 // Persistent grids: the blocks that the SMs hold at once.
-template <int G, int D>
+template <int D>
 void launch_kv_write(const KvParams &p, int sm_count, cudaStream_t cs)
 {
-    const int64_t blocks = (p.rows + 8 * (1024 / D) - 1) / (8 * (1024 / D)), most = static_cast<int64_t>(sm_count) * 4;
-    launch_programmatic(kv_write_kernel<G, D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0,
-                        cs, p);
+    constexpr int rows = 8 * (kWriteThreads / 32);
+    const int64_t blocks = (p.rows + rows - 1) / rows, most = static_cast<int64_t>(sm_count) * 3;
+    launch_programmatic(kv_write_kernel<D>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kWriteThreads),
+                        0, cs, p);
 }
 
 template <int D>
@@ -105,24 +106,10 @@ sdnq_status run_kv(uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int
     p.c_g = rotation_factor(g);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaGetLastError();
-    if (!WRITE) {
+    if (WRITE)
+        D == 128 ? launch_kv_write<128>(p, dev.sm_count, cs) : launch_kv_write<64>(p, dev.sm_count, cs);
+    else
         D == 128 ? launch_kv_read<128>(p, dev.sm_count, cs) : launch_kv_read<64>(p, dev.sm_count, cs);
-    } else if (D == 128) {
-        switch (g) {
-        case 8: launch_kv_write<8, 128>(p, dev.sm_count, cs); break;
-        case 16: launch_kv_write<16, 128>(p, dev.sm_count, cs); break;
-        case 32: launch_kv_write<32, 128>(p, dev.sm_count, cs); break;
-        case 64: launch_kv_write<64, 128>(p, dev.sm_count, cs); break;
-        default: launch_kv_write<128, 128>(p, dev.sm_count, cs); break;
-        }
-    } else {
-        switch (g) {
-        case 8: launch_kv_write<8, 64>(p, dev.sm_count, cs); break;
-        case 16: launch_kv_write<16, 64>(p, dev.sm_count, cs); break;
-        case 32: launch_kv_write<32, 64>(p, dev.sm_count, cs); break;
-        default: launch_kv_write<64, 64>(p, dev.sm_count, cs); break;
-        }
-    }
     return launch_status();
 }
 

@@ -12,10 +12,7 @@
 // read:  x = bf16(butterfly(code) * fp32(s * c)); the butterfly of whole numbers is exact in
 //        fp32 (|sum| <= 128 * 128).
 //
-// Both are bound by memory: 2 D bytes of bf16 and D + 4 bytes of codes and scale per row. In
-// the writer one warp takes 1024 elements = 1024 / D consecutive (token, key-or-value, head) rows at a time
-// with the lane mapping of the rotate+quantize kernel (four 16-byte vectors a lane in flight,
-// fully used 128-byte lines); a row's maximum combines its 8 lanes by shuffles.
+// Both are bound by memory: 2 D bytes of bf16 and D + 4 bytes of codes and scale per row.
 #pragma once
 
 #include "device.cuh"
@@ -80,67 +77,129 @@ __device__ __forceinline__ int64_t kv_held(const KvParams &p, const KvRow &k, in
     return -1;
 }
 
-template <int G, int D>
-__global__ void __launch_bounds__(256, 4) kv_write_kernel(const KvParams p)
+// One row on LANES neighbouring lanes, E consecutive elements each, rotated over groups of g (a
+// run-time power of two from 8 to E LANES) and quantized: the row quantizer's adds, divisions
+// and roundings. Returns the codes, packed, and the row's stored scale.
+template <int E, int LANES>
+__device__ __forceinline__ void quant_row_lanes(float (&v)[E], int32_t g, float c_g, uint32_t lane,
+                                                uint32_t (&codes)[E / 4], float &s)
 {
-    static_assert(D == 64 || D == 128, "head sizes of the cache");
-    constexpr int RPL = 256 / D;        // rows of a lane: 2 (D = 128) or 4 (D = 64)
-    constexpr int VPR = 4 / RPL;        // 64-element vectors of a row
+    static_assert(E >= 8, "groups of 8 and more");
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        const float a = v[i], b = v[i + 1];
+        v[i] = __fadd_rn(a, b);
+        v[i + 1] = __fsub_rn(a, b);
+    }
+#pragma unroll
+    for (int h = 2; h < E; h <<= 1)
+        if (h < 8 || h < g) {
+#pragma unroll
+            for (int i = 0; i < E; i += 2)
+                if ((i & h) == 0)
+                    bfly2(v[i], v[i + 1], v[i + h], v[i + h + 1]);
+        }
+#pragma unroll
+    for (int x = 1; x < LANES; x <<= 1)
+        if (x * E < g) {
+            const float sgn = (lane & x) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const float p0 = __shfl_xor_sync(0xffffffffu, v[i], x), p1 = __shfl_xor_sync(0xffffffffu, v[i + 1], x);
+                fma2(v[i], v[i + 1], v[i], v[i + 1], sgn, sgn, p0, p1);
+            }
+        }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+    for (int x = 1; x < LANES; x <<= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float s_z = __fdiv_rn(m, 127.0f);
+    const bool zero = !(m > 0.0f);
+    float s_q = s_z;
+    if (s_z < 0x1p-126f) {   // a subnormal step: the same quotients, 2^64 times as large on both sides
+        s_q = s_z * 0x1p64f;
+        const float most = s_q * 127.0f;   // (a step rounded down may leave more than 127.5 steps)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            v[i] = fminf(fmaxf(v[i] * 0x1p64f, -most), most);
+    }
+    const float rcp = __frcp_rn(s_q);
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = v[8 * c + i];
+        const uint2 w = quant8(z, s_q, rcp, true);
+        codes[2 * c] = zero ? 0u : w.x;
+        codes[2 * c + 1] = zero ? 0u : w.y;
+    }
+    s = zero ? 0.0f : __fmul_rn(s_z, c_g);
+}
+
+// A warp takes 8 consecutive (token, key or value, head) rows, four lanes a row, so that only
+// the last two stages of the butterfly need shuffles; the next rows' elements are on their way
+// during a row's arithmetic.
+constexpr int kWriteThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kWriteThreads, 3) kv_write_kernel(const KvParams p)
+{
+    constexpr int E = D / 4;
     grid_dependents_launch();
     grid_dependency_wait();
-    const uint32_t lane = lane_id();
-    const int64_t nchunks = (p.rows + 4 * RPL - 1) / (4 * RPL);
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-    for (int64_t c = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-         c < nchunks; c += warps) {
-        const int64_t row0 = c * (4 * RPL) + static_cast<int64_t>(lane >> 3) * RPL;
-        int64_t crow[RPL];
-        uint4 raw[4];
+    const uint32_t lane = lane_id(), t = lane & 3u;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kWriteThreads / 32), step = warps * 8;
+    int64_t row = (static_cast<int64_t>(blockIdx.x) * (kWriteThreads / 32) + (threadIdx.x >> 5)) * 8 + (lane >> 2);
+    const int64_t tiles = (p.rows - (row - (lane >> 2)) + step - 1) / step;   // of this warp
+    KvRow k, k_next = {};
+    int64_t slot, slot_next = -1;
+    uint4 raw[E / 8], raw_next[E / 8];
+    auto fetch = [&] {   // nothing here waits for what it loads
+        slot_next = -1;
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            const uint16_t *x = nullptr;
-            crow[r] = -1;
-            if (row0 + r < p.rows) {
-                const KvRow k = kv_row(p, row0 + r);
-                x = kv_plain(p, k, D);
-                crow[r] = kv_held(p, k, p.slots[k.t]);
-            }
+        for (int i = 0; i < E / 8; ++i)
+            raw_next[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < p.rows) {
+            k_next = kv_row(p, row);
+            slot_next = p.slots[k_next.t];
+            const uint16_t *x = kv_plain(p, k_next, D) + t * E;
 #pragma unroll
-            for (int u = 0; u < VPR; ++u)
-                raw[r * VPR + u] = crow[r] >= 0 ? ld_nc_v4(x + u * 64 + (lane & 7u) * 8)
-                                                : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < E / 8; ++i)
+                raw_next[i] = *reinterpret_cast<const uint4 *>(x + 8 * i);
         }
-        float v[4][8];
+        row += step;
+    };
+    fetch();
+    for (int64_t i = 0; i < tiles; ++i) {
+        k = k_next, slot = slot_next;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            bf16x8_to_f32(raw[t], v[t]);
-        chunk_butterfly<G>(v, lane);
+        for (int c = 0; c < E / 8; ++c)
+            raw[c] = raw_next[c];
+        fetch();
+        float v[E];
 #pragma unroll
-        for (int r = 0; r < RPL; ++r) {
-            float m = 0.0f;
+        for (int c = 0; c < E / 8; ++c) {
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-            for (int u = 0; u < VPR; ++u)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = fmaxf(m, fabsf(v[r * VPR + u][i]));
-#pragma unroll
-            for (int off = 1; off < 8; off <<= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            const float s_z = __fdiv_rn(m, 127.0f);
-            const bool zero = !(m > 0.0f);
-            const bool fast = s_z >= 0x1p-126f;
-            const float rcp = __frcp_rn(s_z);
-            if (crow[r] >= 0) {
-#pragma unroll
-                for (int u = 0; u < VPR; ++u) {
-                    uint2 w = make_uint2(0u, 0u);
-                    if (!zero)
-                        w = quant8(v[r * VPR + u], s_z, rcp, fast);
-                    st_v2(p.codes + crow[r] * D + u * 64 + (lane & 7u) * 8, w.x, w.y);
-                }
-                if ((lane & 7u) == 0u)
-                    p.scales[crow[r]] = zero ? 0.0f : __fmul_rn(s_z, p.c_g);
+            for (int u = 0; u < 4; ++u) {
+                v[8 * c + 2 * u] = __uint_as_float(w[u] << 16);
+                v[8 * c + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
             }
+        }
+        uint32_t codes[E / 4];
+        float s;
+        quant_row_lanes<E, 4>(v, p.group, p.c_g, lane, codes, s);
+        const int64_t crow = kv_held(p, k, slot);
+        if (crow >= 0) {
+#pragma unroll
+            for (int c = 0; c < E / 4; c += 4)
+                st_v4(p.codes + crow * D + t * E + 4 * c, codes[c], codes[c + 1], codes[c + 2], codes[c + 3]);
+            if (t == 0u)
+                p.scales[crow] = s;
         }
     }
 }
