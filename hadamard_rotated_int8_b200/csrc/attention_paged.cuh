@@ -30,6 +30,7 @@ struct PagedParams {
     int64_t pages;
     int32_t T, B, H, Hkv;
     int32_t share;           // H / Hkv
+    uint32_t share_mul, share_shift;   // n / share = n * share_mul >> share_shift for 0 <= n < 2^31
     int32_t page_shift;
     int32_t cap;             // most keys a table row can name
     int32_t window;          // <= 0: none
@@ -43,6 +44,19 @@ struct PagedParams {
     void *desc;
     uint64_t timeout_ns;
 };
+
+__device__ __forceinline__ int32_t by_share(const PagedParams &p, int32_t n)
+{
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * p.share_mul) >> p.share_shift);
+}
+
+// a / b, in 32 bits where they hold both (a division in 64 takes several times as long).
+__device__ __forceinline__ int64_t div_wide(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // A sequence as the device arrays give it, made safe: rows [q0, q0 + n) lie in [0, T), the
 // length lies in [0, cap]. What had to be changed is recorded in the device error word.
@@ -96,33 +110,6 @@ __device__ __forceinline__ void warp_butterfly(float (&v)[E], int32_t g, uint32_
         }
 }
 
-// Codes (packed little-endian) and scale of one row held by a warp as above.
-template <int E>
-__device__ __forceinline__ uint32_t warp_quant_row(float (&v)[E], int32_t g, float c_g,
-                                                   uint32_t lane, float &s)
-{
-    warp_butterfly(v, g, lane);
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        m = fmaxf(m, fabsf(v[i]));
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float s_z = __fdiv_rn(m, 127.0f);
-    const bool zero = !(m > 0.0f);
-    uint32_t w = 0u;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float t = zero ? 0.0f : __fdiv_rn(v[i], s_z);
-        const float r = fminf(fmaxf(rintf(t), -127.0f), 127.0f);
-        const int32_t code = t == t ? __float2int_rn(r) : 0;
-        w |= (static_cast<uint32_t>(code) & 0xffu) << (8 * i);
-    }
-    s = zero ? 0.0f : __fmul_rn(s_z, c_g);
-    return w;
-}
-
 // ---------------------------------------------------------------- work split
 //
 // A segment is one (sequence, kv head, tile of query rows); the rows of a tile are (token,
@@ -152,7 +139,7 @@ __device__ __forceinline__ int32_t paged_qtiles(const PagedParams &p, const Page
 template <int TILE, int ROWS>
 __device__ __forceinline__ PagedTiles paged_tiles(const PagedParams &p, int32_t n, int32_t len, int32_t q)
 {
-    const int32_t first = q * ROWS / p.share, last = min(q * ROWS + ROWS - 1, n * p.share - 1) / p.share;
+    const int32_t first = by_share(p, q * ROWS), last = by_share(p, min(q * ROWS + ROWS - 1, n * p.share - 1));
     const int32_t end = max(len - n + last + 1, 0);   // keys [0, end) are in reach
     const int32_t low = p.window > 0 ? max(0, len - n + first - p.window + 1) : 0;
     PagedTiles t;
@@ -200,8 +187,8 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t v, uint32_t lane)
     return v;
 }
 
-// The tiles of the 32 sequences b (one a lane): a sequence of up to 2 query tiles is its
-// lane's work, longer ones are walked by the whole warp.
+// The tiles that a head of the 32 sequences b (one a lane) has: a sequence of up to 2 query
+// tiles is its lane's work, longer ones are walked by the whole warp.
 template <int TILE, int ROWS>
 __device__ __forceinline__ int64_t sequence_tiles(const PagedParams &p, int32_t b, uint32_t lane, PagedSeq &s,
                                                   int32_t &qt)
@@ -225,11 +212,11 @@ __device__ __forceinline__ int64_t sequence_tiles(const PagedParams &p, int32_t 
         if (static_cast<int>(lane) == src)
             sum += part;
     }
-    return sum * p.Hkv;
+    return sum;
 }
 
 // Counts the list's tiles (the whole block), and finds where share blockIdx.x of `blocks`
-// begins: tile `first` of `total`, shares of `per` >= `least` tiles. `found`: 4 words of shared
+// begins: tile `first` of `total`, shares of `per` >= `least` tiles. `found`: 8 words of shared
 // memory.
 template <int TILE, int ROWS, int THREADS>
 __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks, int32_t least, int32_t *found,
@@ -243,14 +230,17 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
     const int32_t g0 = min(warp * each, groups), g1 = min(g0 + each, groups);
     PagedSeq s;
     int32_t qt;
-    int64_t sum = 0;
-    for (int32_t g = g0; g < g1; ++g)
-        sum += sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
-    sum = __shfl_sync(0xffffffffu, warp_inclusive_sum(sum, lane), 31);
+    int64_t mine = 0, incl = 0, sum = 0;   // of the last group looked at; of all
+#pragma unroll 1
+    for (int32_t g = g0; g < g1; ++g) {
+        mine = sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
+        incl = warp_inclusive_sum(mine, lane);
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
     if (lane == 0)
         warp_sum[warp] = sum;
     __syncthreads();
-    int64_t before = 0;
+    int64_t before = 0;   // tiles of a head, as the sums are; a sequence's heads follow each other
     total = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
@@ -258,28 +248,33 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
             before += warp_sum[i];
         total += warp_sum[i];
     }
-    per = (total + blocks - 1) / blocks;
+    before *= p.Hkv, sum *= p.Hkv, total *= p.Hkv;
+    per = div_wide(total + blocks - 1, blocks);
     per = per < least ? least : per;
     first = static_cast<int64_t>(blockIdx.x) * per;
     if (first < total && first >= before && first < before + sum) {   // one warp
         int64_t rest = first - before;
+#pragma unroll 1
         for (int32_t g = g0; g < g1; ++g) {
-            const int64_t mine = sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
-            const int64_t incl = warp_inclusive_sum(mine, lane);
-            const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+            if (g1 - g0 > 1) {
+                mine = sequence_tiles<TILE, ROWS>(p, g * 32 + static_cast<int32_t>(lane), lane, s, qt);
+                incl = warp_inclusive_sum(mine, lane);
+            }
+            const int64_t all = __shfl_sync(0xffffffffu, incl, 31) * p.Hkv;
             if (rest >= all) {
                 rest -= all;
                 continue;
             }
-            const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, rest < incl))) - 1;
+            const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, rest < incl * p.Hkv))) - 1;
             const int32_t n = __shfl_sync(0xffffffffu, s.n, src), len = __shfl_sync(0xffffffffu, s.len, src);
-            const int32_t qn = __shfl_sync(0xffffffffu, qt, src);
-            const int64_t head = __shfl_sync(0xffffffffu, mine, src) / p.Hkv;
-            rest -= __shfl_sync(0xffffffffu, incl - mine, src);
-            const int64_t kvh = rest / head;
+            const int32_t qn = __shfl_sync(0xffffffffu, qt, src), q0 = __shfl_sync(0xffffffffu, s.q0, src);
+            const int64_t head = __shfl_sync(0xffffffffu, mine, src);
+            rest -= __shfl_sync(0xffffffffu, incl - mine, src) * p.Hkv;
+            const int64_t kvh = div_wide(rest, head);
             rest -= kvh * head;
-            for (int32_t q0 = 0; q0 < qn; q0 += 32) {
-                const int32_t q = q0 + static_cast<int32_t>(lane);
+#pragma unroll 1
+            for (int32_t t0 = 0; t0 < qn; t0 += 32) {
+                const int32_t q = t0 + static_cast<int32_t>(lane);
                 const int64_t nt = q < qn ? paged_tiles<TILE, ROWS>(p, n, len, q).nt : 0;
                 const int64_t qi = warp_inclusive_sum(nt, lane);
                 const int64_t qall = __shfl_sync(0xffffffffu, qi, 31);
@@ -292,8 +287,9 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
                 if (lane == 0) {
                     found[0] = g * 32 + src;
                     found[1] = static_cast<int32_t>(kvh);
-                    found[2] = q0 + at;
+                    found[2] = t0 + at;
                     found[3] = static_cast<int32_t>(rest);
+                    found[4] = q0, found[5] = n, found[6] = len, found[7] = qn;
                 }
                 break;
             }
@@ -304,8 +300,7 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
     w.b = 0, w.kvh = 0, w.q = 0, w.i = 0, w.qt = 0;
     if (first < total) {
         w.b = found[0], w.kvh = found[1], w.q = found[2], w.i = found[3];
-        w.s = paged_seq(p, w.b);
-        w.qt = paged_qtiles<ROWS>(p, w.s);
+        w.s.q0 = found[4], w.s.n = found[5], w.s.len = found[6], w.qt = found[7];
         w.t = paged_tiles<TILE, ROWS>(p, w.s.n, w.s.len, w.q);
     }
 }
@@ -354,7 +349,7 @@ struct FewConfig {
     static constexpr int BAR_OFF = ML_OFF + 4 * ROWS * 8;
     static constexpr int META_OFF = BAR_OFF + 2 * NST * 8;      // valid boxes of each stage
     static constexpr int SCAN_OFF = META_OFF + 16;
-    static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 16;
+    static constexpr int SMEM_BYTES = 1024 + SCAN_OFF + 32;
     static_assert(BAR_OFF % 8 == 0 && META_OFF % 4 == 0 && NST * 4 <= 16 &&
                       PER_SM * (SMEM_BYTES + 1024 + 128) <= 228 * 1024,
                   "shared memory per SM");
@@ -594,47 +589,35 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
         const int32_t r0 = w.q * ROWS, head0 = w.kvh * p.share;
         const int32_t rows = min(ROWS, w.s.n * p.share - r0);
         const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
-        // query rows warp, warp + 4, ...: codes and scales (rows past the last: zeros)
+        // the query rows' codes and scales (rows past the last: zeros)
         {
-            constexpr int RQ = ROWS / 4;
-            uint32_t x[RQ][E / 2];
+            constexpr int LANES = D == 128 && NB == 1 ? 16 : 8, QE = D / LANES;   // of a row; elements of a lane
+            const int32_t lr = static_cast<int32_t>(warp) * (32 / LANES) + static_cast<int32_t>(lane) / LANES, r = r0 + lr;
+            if (static_cast<int32_t>(warp) * (32 / LANES) < ROWS) {
+                const uint32_t at = lane % LANES * QE;
+                float v[QE];
 #pragma unroll
-            for (int rr = 0; rr < RQ; ++rr) {
-                const int32_t lr = rr * 4 + static_cast<int32_t>(warp), r = r0 + lr;
+                for (int i = 0; i < QE / 8; ++i) {
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u);
+                    if (lr < rows) {
+                        const int32_t ti = by_share(p, r);
+                        a = ld_nc_v4(p.q + static_cast<int64_t>(w.s.q0 + ti) * p.ldq +
+                                     static_cast<int64_t>(head0 + r - ti * p.share) * D + at + 8 * i);
+                    }
+                    const uint32_t x[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i)
-                    x[rr][i] = 0u;
-                if (lr < rows) {
-                    const int32_t ti = r / p.share;
-                    const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + ti) * p.ldq +
-                                        static_cast<int64_t>(head0 + r - ti * p.share) * D + lane * E;
-                    if (E == 4) {
-                        const uint2 a = *reinterpret_cast<const uint2 *>(q);
-                        x[rr][0] = a.x, x[rr][E / 2 - 1] = a.y;
-                    } else {
-                        x[rr][0] = *reinterpret_cast<const uint32_t *>(q);
+                    for (int u = 0; u < 4; ++u) {
+                        v[8 * i + 2 * u] = __uint_as_float(x[u] << 16);
+                        v[8 * i + 2 * u + 1] = __uint_as_float(x[u] & 0xffff0000u);
                     }
                 }
-            }
+                uint32_t codes[QE / 4];
+                float sq;
+                quant_row_lanes<QE, LANES>(v, p.group, p.c_g, lane, codes, sq);
 #pragma unroll
-            for (int rr = 0; rr < RQ; ++rr) {
-                const int32_t lr = rr * 4 + static_cast<int32_t>(warp);
-                uint32_t c = 0u;
-                float sq = 0.0f;
-                if (lr < rows) {
-                    float v[E];
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) {
-                        v[2 * i] = __uint_as_float(x[rr][i] << 16);
-                        v[2 * i + 1] = __uint_as_float(x[rr][i] & 0xffff0000u);
-                    }
-                    c = warp_quant_row<E>(v, p.group, p.c_g, lane, sq);
-                }
-                if (E == 4)
-                    *reinterpret_cast<uint32_t *>(smem + C::Q_OFF + lr * D + lane * E) = c;
-                else
-                    *reinterpret_cast<uint16_t *>(smem + C::Q_OFF + lr * D + lane * E) = static_cast<uint16_t>(c);
-                if (lane == 0)
+                for (int i = 0; i < QE / 4; ++i)
+                    *reinterpret_cast<uint32_t *>(smem + C::Q_OFF + lr * D + at + 4 * i) = codes[i];
+                if (lane % LANES == 0)
                     qs[lr] = sq;
             }
         }
@@ -652,12 +635,12 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                 const int32_t lr = 8 * nb + 2 * static_cast<int32_t>(t) + c;
                 // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out (attention.cuh)
                 row_f[nb][c] = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
-                pos[nb][c] = w.s.len - w.s.n + (r0 + min(lr, rows - 1)) / p.share;
+                pos[nb][c] = w.s.len - w.s.n + by_share(p, r0 + min(lr, rows - 1));
                 low[nb][c] = p.window > 0 ? pos[nb][c] - p.window + 1 : INT32_MIN;
             }
         }
-        const int32_t pos_first = w.s.len - w.s.n + r0 / p.share;
-        const int32_t pos_last = w.s.len - w.s.n + (r0 + rows - 1) / p.share;
+        const int32_t pos_first = w.s.len - w.s.n + by_share(p, r0);
+        const int32_t pos_last = w.s.len - w.s.n + by_share(p, r0 + rows - 1);
         const int32_t low_first = p.window > 0 ? pos_first - p.window + 1 : INT32_MIN;
         const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : INT32_MIN;
         float m[NB][2], l[NB][2];
@@ -882,7 +865,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
 #pragma unroll
             for (int i = 0; i < E; ++i)
                 v[i] = obuf[lr * C::O_LD + lane * E + i];
-            const int32_t r = r0 + lr, tok = r / p.share;
+            const int32_t r = r0 + lr, tok = by_share(p, r);
             if (begins && ends) {
                 if (ok)
                     paged_store_row<D>(p, v, ll, w.s.q0 + tok, head0 + r - tok * p.share, lane);
@@ -954,7 +937,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedPara
                 v[i] = __fmaf_rn(a[i], fn, v[i] * fo);
             m = mn;
         }
-        const int32_t r = d.r0 + lr, tok = r / p.share;
+        const int32_t r = d.r0 + lr, tok = by_share(p, r);
         if (W == 1) {
             paged_store_row<D>(p, v, l, d.q0 + tok, d.head0 + r - tok * p.share, lane);
             continue;

@@ -46,7 +46,7 @@ struct ChunkConfig {
     static constexpr int NBARS = 2 * (NK + NV + NB) + 8 + 2 + 1;
     static constexpr int META_OFF = BAR_OFF + NBARS * 8;    // valid boxes of each scale stage
     static constexpr int HOLD_OFF = META_OFF + NS * 4;      // TMEM address, abort flag, scan result
-    static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 32;
+    static constexpr int SMEM_BYTES = 1024 + HOLD_OFF + 48;
     static_assert((NK & (NK - 1)) == 0 && (NB & (NB - 1)) == 0, "ring positions are masked");
     // step h is loaded once P(h - NK - 1) is written, so that step h - NS - 1 and older are read
     static_assert(NS >= NK + 2 && (NS & (NS - 1)) == 0, "the scales need no barriers of their own");
@@ -439,12 +439,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
             }
-            const int32_t tok = (r0 + min(lr, rows - 1)) / p.share;
+            const int32_t tok = by_share(p, r0 + min(lr, rows - 1));
             const int32_t pos0 = w.s.len - w.s.n;
             const int32_t pos = pos0 + tok, low = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
             // the tile's first and last row: which steps are wholly visible
-            const int32_t pos_first = pos0 + (r0 + static_cast<int32_t>(tile) * 128) / p.share;
-            const int32_t pos_last = pos0 + (r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1)) / p.share;
+            const int32_t pos_first = pos0 + by_share(p, r0 + static_cast<int32_t>(tile) * 128);
+            const int32_t pos_last = pos0 + by_share(p, r0 + min(static_cast<int32_t>(tile) * 128 + 127, rows - 1));
             const int32_t low_last = p.window > 0 ? pos_last - p.window + 1 : 0;
             // this warp's 32 query rows, four at a time: rotated, quantized, into the operand
             // tile; the next four's elements are on their way meanwhile
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const int32_t row0 = static_cast<int32_t>(quad * 32u + (lane >> 3));
                 auto load = [&](int32_t it, uint4 (&x)[V]) {
                     const int32_t row = static_cast<int32_t>(tile) * 128 + row0 + it * 4;
-                    const int32_t tk = (r0 + row) / p.share;
+                    const int32_t tk = by_share(p, r0 + row);
                     const uint16_t *q = p.q + static_cast<int64_t>(w.s.q0 + tk) * p.ldq +
                                         static_cast<int64_t>(w.kvh * p.share + r0 + row - tk * p.share) * D + (lane & 7u) * E;
 #pragma unroll

@@ -260,6 +260,9 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     p.H = static_cast<int32_t>(H);
     p.Hkv = static_cast<int32_t>(Hkv);
     p.share = static_cast<int32_t>(H / Hkv);
+    const int32_t bits = log2_of(p.share);   // division by the share as a product (rounded up)
+    p.share_shift = static_cast<uint32_t>(31 + bits);
+    p.share_mul = static_cast<uint32_t>(((1ull << p.share_shift) + p.share - 1) / p.share);
     p.page_shift = log2_of(page);
     p.cap = static_cast<int32_t>(max_pages * page);
     p.window = static_cast<int32_t>(window < kPagedMaxKeys ? window : kPagedMaxKeys);
