@@ -490,6 +490,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
+        fence_proxy_async_global();   // the kernel before may have stored the rows that the copies read
         int64_t n = 0;
         uint32_t st = 0, phase = 1;
         bool ok = true;
@@ -938,35 +939,35 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const PagedPara
             m = mn;
         }
         const int32_t r = d.r0 + lr, tok = by_share(p, r);
-        if (W == 1) {
+        if constexpr (W == 1) {
             paged_store_row<D>(p, v, l, d.q0 + tok, d.head0 + r - tok * p.share, lane);
-            continue;
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            part[warp % W][lane * E + i] = v[i];
-        if (lane == 0)
-            part_ml[warp % W] = make_float2(m, l);
-        __syncthreads();
-        if (warp == 0) {
-            float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                mm = fmaxf(mm, part_ml[i].x);
+        } else {
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                v[i] = 0.0f;
+                part[warp][lane * E + i] = v[i];
+            if (lane == 0)
+                part_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp == 0) {
+                float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const float f = part_ml[k].x == -INFINITY ? 0.0f : ex2_approx(part_ml[k].x - mm);
-                ll = __fmaf_rn(part_ml[k].y, f, ll);
+                for (int i = 0; i < W; ++i)
+                    mm = fmaxf(mm, part_ml[i].x);
 #pragma unroll
                 for (int i = 0; i < E; ++i)
-                    v[i] = __fmaf_rn(part[k][lane * E + i], f, v[i]);
+                    v[i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    const float f = part_ml[k].x == -INFINITY ? 0.0f : ex2_approx(part_ml[k].x - mm);
+                    ll = __fmaf_rn(part_ml[k].y, f, ll);
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        v[i] = __fmaf_rn(part[k][lane * E + i], f, v[i]);
+                }
+                paged_store_row<D>(p, v, ll, d.q0 + tok, d.head0 + r - tok * p.share, lane);
             }
-            paged_store_row<D>(p, v, ll, d.q0 + tok, d.head0 + r - tok * p.share, lane);
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 

@@ -9,10 +9,10 @@
 // - warp 1 issues S_t = Q_t K^T (tcgen05 kind::i8, int32 in TMEM) three steps ahead of
 //   O_t += P_t V (kind::f16, fp32 in TMEM): logits and P of a tile have two buffers each, so
 //   that its softmax never waits for a product just issued. A commit costs the issuing warp
-//   about 200 cycles and a wait 110 or more, so there is one commit a tile and step: `done` of
-//   iteration k covers S(k) and P(k - 3) V(k - 3), and the rest follows from the softmax's
-//   "P(k - 3) written": S(k - 2) is done with K(k - 2) and has been read, the scales of step
-//   k - 3 have been read, P(k - 5) V(k - 5) is done;
+//   about 200 cycles and a wait 110 or more, so there is one commit a tile and step, and one
+//   that frees V(k - 3): `done` of iteration k covers S(k) and P(k - 3) V(k - 3), and the rest
+//   follows from the softmax's "P(k - 3) written": S(k - 2) is done with K(k - 2) and has been
+//   read, and so have the scales of step k - 3;
 // - warps 4..7 (tile 0) and 8..11 (tile 1), one thread a query row, rotate and quantize their
 //   query rows into the operand tile, then per step form 64 base-2 logits, an online softmax
 //   (sums rescaled only when the maximum grows by more than 8), and P = probability * s_v in
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
+        fence_proxy_async_global();   // the kernel before may have stored the rows that the copies read
         uint32_t ks = 0, kph = 1, vs = 0, vph = 1, ss = 0;
         int64_t n = 0, issued = 0;
         while (ok && n < count) {
@@ -306,82 +307,85 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         drain(v_full(0), NV);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
-        // The whole warp walks the loops, so that descriptors stay in uniform registers; one lane
-        // issues.
-        const bool leader = elect_one();
-        constexpr uint32_t IDESC_S = idesc_s8_s32(128, 64);
-        constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
-        // operand descriptors; 16 bytes further on is 1 more
-        const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
-        const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
-        // steps of all pieces so far, and of each tile's pieces
-        uint32_t c0 = 0, g0 = 0, g1 = 0;
-        int64_t n = 0;
-        while (n < count) {
-            const int32_t steps = piece_steps(n);
-            const uint32_t in_use = piece_rows() > 128 ? 2 : 1;
-            // iteration k: S(k) goes out when P(k - 3) is written (S(k - 2), its buffer's last, has
-            // been read then), just before the product of that P with V
-#pragma unroll 1
-            for (int32_t k = 0; k < steps + 3; ++k) {
-                const uint32_t c = c0 + static_cast<uint32_t>(k), ks = c % NK, bs = (c - 3u) % NB;   // ring positions
-                const bool s_now = k < steps, pv_now = k >= 3;
-                if (s_now && pv_now)
-                    wait2(k_full(ks), (c / NK) & 1u, b_full(bs), ((c - 3u) / NB) & 1u);
-                else if (s_now)
-                    wait(k_full(ks), (c / NK) & 1u);
-                else if (pv_now)
-                    wait(b_full(bs), ((c - 3u) / NB) & 1u);
-#pragma unroll 1
-                for (uint32_t t = 0; t < in_use; ++t) {
-                    const uint32_t g = (t == 0 ? g0 : g1) + static_cast<uint32_t>(k), b = g & 1u;
-                    if (pv_now)
-                        wait(p_full(t, b ^ 1u), ((g - 3u) >> 1) & 1u);
-                    else if (k == 0 || k == 2)   // Q is there; S(0) has been read
-                        wait(q_full(t), static_cast<uint32_t>(k) >> 1);
-                    tc_fence_after_sync();
+        // One thread's work. What an iteration waits for is tried at once: a ready barrier takes 110
+        // cycles and more to say so.
+        if (elect_one()) {
+            constexpr uint32_t IDESC_S = idesc_s8_s32(128, 64);
+            constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, true);
+            // operand descriptors; 16 bytes further on is 1 more
+            const uint64_t dq = codes_desc<D>(base + C::Q_OFF), dk = codes_desc<D>(base + C::K_OFF);
+            const uint64_t dp = kmajor_desc(base + C::P_OFF), db = mnmajor_desc(base + C::B_OFF, 8192);
+            // steps of all pieces so far, and of each tile's pieces
+            uint32_t c0 = 0, g0 = 0, g1 = 0;
+            int64_t n = 0;
+            auto need = [&](bool got, uint32_t bar, uint32_t parity) {
+                if (ok && !got)
+                    ok = mbar_wait_tries(bar, parity, abort);
+            };
+            while (n < count) {
+                const int32_t steps = piece_steps(n);
+                const bool two = piece_rows() > 128;
+                auto issue = [&](uint32_t t, uint32_t b, uint32_t ks, uint32_t bs, bool s_now, bool pv_now, bool pv_first) {
                     const uint64_t qa = dq + t * (C::Q_TILE >> 4), ka = dk + ks * (C::K_STAGE >> 4);
                     const uint64_t pa = dp + (2 * t + (b ^ 1u)) * (C::P_BUF >> 4), va = db + bs * (C::B_STAGE >> 4);
-                    if (leader) {
-                        if (s_now) {
+                    if (s_now) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 32; ++kk)
-                                mma_s8(tmem_base + t * 128 + b * 64, qa + 2 * kk, ka + 2 * kk, IDESC_S, kk != 0 ? 1u : 0u);
-                        }
-                        if (pv_now) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, k > 3 || kk != 0 ? 1u : 0u);
-                        }
-                        tc_commit(done(t, b));
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            mma_s8(tmem_base + t * 128 + b * 64, qa + 2 * kk, ka + 2 * kk, IDESC_S, kk != 0 ? 1u : 0u);
                     }
-                    __syncwarp();
-                }
-                if (leader && pv_now) {
-                    if (k == 3)
-                        mbar_arrive(k_empty((c - 3u) % NK));
-                    if (k < steps + 2)
-                        mbar_arrive(k_empty((c - 2u) % NK));
-                    if (k >= 5)
-                        mbar_arrive(b_empty((c - 5u) % NB));
-                    if (k == steps + 2) {
-                        if (steps > 1)
-                            tc_commit(b_empty((c - 4u) % NB));
+                    if (pv_now) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, !pv_first || kk != 0 ? 1u : 0u);
+                    }
+                    tc_commit(done(t, b));
+                };
+                // iteration k: S(k) goes out when P(k - 3) is written (S(k - 2), its buffer's last, has
+                // been read then), just before the product of that P with V
+#pragma unroll 1
+                for (int32_t k = 0; k < steps + 3; ++k) {
+                    const uint32_t c = c0 + static_cast<uint32_t>(k), ks = c % NK, bs = (c - 3u) % NB;   // ring positions
+                    const bool s_now = k < steps, pv_now = k >= 3;
+                    const uint32_t x0 = g0 + static_cast<uint32_t>(k), x1 = g1 + static_cast<uint32_t>(k), b0 = x0 & 1u, b1 = x1 & 1u;
+                    const uint32_t k_par = (c / NK) & 1u, b_par = ((c - 3u) / NB) & 1u;
+                    // P(k - 3); before that, Q (k = 0) and "S(0) has been read" (k = 2)
+                    const uint32_t bar0 = pv_now ? p_full(0, b0 ^ 1u) : q_full(0), bar1 = pv_now ? p_full(1, b1 ^ 1u) : q_full(1);
+                    const uint32_t par0 = pv_now ? ((x0 - 3u) >> 1) & 1u : static_cast<uint32_t>(k) >> 1;
+                    const uint32_t par1 = pv_now ? ((x1 - 3u) >> 1) & 1u : static_cast<uint32_t>(k) >> 1;
+                    const bool got_k = mbar_try_wait(k_full(ks), k_par), got_b = mbar_try_wait(b_full(bs), b_par);
+                    const bool got_0 = mbar_try_wait(bar0, par0), got_1 = mbar_try_wait(bar1, par1);
+                    if (s_now)
+                        need(got_k, k_full(ks), k_par);
+                    if (pv_now)
+                        need(got_b, b_full(bs), b_par);
+                    if (k != 1)
+                        need(got_0, bar0, par0);
+                    tc_fence_after_sync();
+                    issue(0, b0, ks, bs, s_now, pv_now, k == 3);
+                    if (two) {
+                        if (k != 1)
+                            need(got_1, bar1, par1);
+                        tc_fence_after_sync();
+                        issue(1, b1, ks, bs, s_now, pv_now, k == 3);
+                    }
+                    if (pv_now) {
                         tc_commit(b_empty(bs));
+                        if (k == 3)
+                            mbar_arrive(k_empty((c - 3u) % NK));
+                        if (k < steps + 2)
+                            mbar_arrive(k_empty((c - 2u) % NK));
                     }
                 }
-                __syncwarp();
+                c0 += static_cast<uint32_t>(steps);
+                g0 += static_cast<uint32_t>(steps);
+                g1 += two ? static_cast<uint32_t>(steps) : 0u;
+                n += steps;
+                walk_next_segment<kChunkTile, kChunkRows>(p, w);
             }
-            c0 += static_cast<uint32_t>(steps);
-            g0 += static_cast<uint32_t>(steps);
-            g1 += in_use == 2 ? static_cast<uint32_t>(steps) : 0u;
-            n += steps;
-            walk_next_segment<kChunkTile, kChunkRows>(p, w);
-        }
-        if (leader) {
             tc_commit(drain_bar);
             mbar_wait_tries(drain_bar, 0u, abort);
         }
+        __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------------ value codes to bf16
         // Eight lanes take four 16-byte chunks of the keys k and k ^ 5: the swizzles put both
@@ -515,15 +519,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 return false;
             };
-            // acc * s_k of 4 columns; fp32(acc) without the conversion pipe (attention.cuh)
+            // acc * s_k of 4 columns (converting takes one instruction an element here; adding the
+            // magic number and subtracting it again, one and a half: 659 against 646 us for a chunk
+            // of 2048 over 16384 keys, 32 heads over 8)
             auto scale4 = [&](const uint32_t *acc, float *y, uint32_t at) {
                 const float4 k4 = lds_v4(at);   // a broadcast
                 float f[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    f[u] = __uint_as_float(acc[u] + 0x4B400000u);
-                sub2(f[0], f[1], f[0], f[1], 12582912.0f, 12582912.0f);
-                sub2(f[2], f[3], f[2], f[3], 12582912.0f, 12582912.0f);
+                    f[u] = static_cast<float>(static_cast<int32_t>(acc[u]));
                 mul2(y[0], y[1], f[0], f[1], k4.x, k4.y);
                 mul2(y[2], y[3], f[2], f[3], k4.z, k4.w);
             };

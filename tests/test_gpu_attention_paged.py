@@ -377,3 +377,46 @@ def test_more_query_rows_than_a_grid_dimension():
                             np.arange(41), 256, 0.125)
     check(out[:40], o, size, 16)
     assert torch.equal(out, out[:40][torch.arange(B, device="cuda") % 40])
+
+
+@pytest.mark.parametrize("share,D,window,sinks", [(1, 128, 70, 0), (1, 64, 40, 130), (3, 128, 10, 3), (1, 128, 0, 0)])
+def test_short_chunks_of_many_lengths(share, D, window, sinks):
+    """Chunks whose key ranges are a few steps long, tiles with and without a second half, several to a block, with
+    single tokens and empty sequences in between."""
+    rng = np.random.default_rng(share + D)
+    B, Hkv, page = 150, 2, 16
+    new = rng.choice([0, 1, 2, 33, 40, 65, 127, 128, 129, 200, 256, 257, 300], B)
+    lens = new + rng.choice([0, 1, 15, 64, 90], B)
+    cache = ref.Cache(Hkv, page, D, ref.pages_of(lens, page), 41, group=64)
+    cu = ref.offsets(new)
+    q = ref.queries(int(cu[-1]), share * Hkv, D, 42)
+    out = call(q, cache.gpu(), lens, cu, int(new.max()), window=window, sinks=sinks, group=64)
+    assert sd.sdnq_device_status() == 0
+    for b in rng.permutation(B)[:25]:
+        n, L, t = int(new[b]), int(lens[b]), int(cu[b])
+        for i in sorted({0, n // 2, 127, 128, n - 1} & set(range(n))):
+            at = L - n + i      # row i sees what the last row of a context of at + 1 keys sees
+            o, size = ref.attention(q[t + i:t + i + 1], cache.codes, cache.scales, cache.table[b:b + 1], [at + 1], [0, 1],
+                                    64, D ** -0.5, window, sinks)
+            check(out[t + i:t + i + 1], o, size, 400)
+    assert torch.equal(out, call(q, cache.gpu(), lens, cu, int(new.max()), window=window, sinks=sinks, group=64))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls that overlap on the GPU, each with its own workspace, in both forms."""
+    lens, new = [3000, 700, 90], [400, 1, 33]
+    cache = ref.Cache(2, 16, 128, ref.pages_of(lens, 16), 51)
+    gpu = cache.gpu()
+    gl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    gc = torch.from_numpy(ref.offsets(new)).cuda()
+    q1, q2 = ref.queries(434, 8, 128, 1).cuda(), ref.queries(3, 8, 128, 2).cuda()
+    want1 = sd.sdnq_attention_paged(q1, *gpu, gl, cu_q=gc, max_q=400)
+    want2 = sd.sdnq_attention_paged(q2, *gpu, gl)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        got.append((sd.sdnq_attention_paged(q1, *gpu, gl, cu_q=gc, max_q=400, stream=a), want1))
+        got.append((sd.sdnq_attention_paged(q2, *gpu, gl, stream=b), want2))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
