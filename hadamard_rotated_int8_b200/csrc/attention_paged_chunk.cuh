@@ -93,9 +93,9 @@ __device__ __forceinline__ void thread_butterfly(float (&v)[D], int32_t g)
 
 // Waits for a phase in a handful of instructions (the loops of this kernel's roles share one
 // instruction cache, and mbar_wait_bounded's clock costs six times the code). Gives up after
-// `kWaitTries` tries (each up to about a microsecond where the hardware suspends the thread):
-// then it raises `abort` and the device error word and returns false.
-constexpr uint32_t kWaitTries = 1u << 21;
+// kWaitTries tries, about 2 s (the hardware suspends the thread for 4 us each): then it raises
+// `abort` and the device error word and returns false.
+constexpr uint32_t kWaitTries = 1u << 19;
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, volatile int *abort)
 {
     uint32_t done;
