@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             };
             // The loop handles a step's exponentials together with the scaling of the next one's
             // logits, column by column in the same registers: the two use different pipes.
-            uint32_t acc[32];
+            uint32_t acc[16];
             auto next_done = [&](uint32_t b) {   // (none may be left out: a wait sees only the parity)
                 wait(done(tile, b), (parity >> b) & 1u);
                 parity ^= 1u << b;
@@ -559,12 +559,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_fence_after_sync();
             bool whole = look(0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                tmem_ld_32x32b_x32(s_addr + (g & 1u) * 64u + h * 32u, acc);
+            for (int h = 0; h < 4; ++h) {
+                tmem_ld_32x32b_x16(s_addr + (g & 1u) * 64u + h * 16u, acc);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    scale4(acc + e, y + h * 32 + e, base + C::SC_OFF + (n0 % NS) * 512u + (h * 32 + e) * 4);
+                for (int e = 0; e < 16; e += 4)
+                    scale4(acc + e, y + h * 16 + e, base + C::SC_OFF + (n0 % NS) * 512u + (h * 16 + e) * 4);
             }
             if (!whole)
                 hide();
@@ -593,13 +593,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         wait(done(tile, b), (parity >> b) & 1u);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int32_t c = 0; c < D; c += 32) {
-                            tmem_ld_32x32b_x32(o_addr + c, acc);
+                        for (int32_t c = 0; c < D; c += 16) {
+                            tmem_ld_32x32b_x16(o_addr + c, acc);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                acc[e] = __float_as_uint(__uint_as_float(acc[e]) * alpha);
-                            tmem_st_32x32b_x32(o_addr + c, acc);
+                            for (int e = 0; e < 16; e += 4) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    x[u] = __float_as_uint(__uint_as_float(acc[e + u]) * alpha);
+                                tmem_st_32x32b_x4(o_addr + c + e, x);
+                            }
                         }
                         tmem_st_wait();
                     }
@@ -612,23 +616,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld_32x32b_x32(s_addr + (b ^ 1u) * 64u + h * 32u, acc);   // (of the last step: not used)
+                for (int h = 0; h < 4; ++h) {
+                    tmem_ld_32x32b_x16(s_addr + (b ^ 1u) * 64u + h * 16u, acc);   // (of the last step: not used)
                     tmem_ld_wait();
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
+                    for (int ch = 0; ch < 2; ++ch) {
                         uint32_t x[4];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            float *z = y + h * 32 + ch * 8 + q * 4;
-                            const float4 v4 = lds_v4(svb + (h * 32 + ch * 8 + q * 4) * 4);
+                            float *z = y + h * 16 + ch * 8 + q * 4;
+                            const float4 v4 = lds_v4(svb + (h * 16 + ch * 8 + q * 4) * 4);
                             float f[4];
                             fma2(f[0], f[1], z[0], z[1], row_f, row_f, neg_m, neg_m);
                             fma2(f[2], f[3], z[2], z[3], row_f, row_f, neg_m, neg_m);
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
                                 f[u] = ex2_approx(f[u]);
-                            scale4(acc + ch * 8 + q * 4, z, skb + (h * 32 + ch * 8 + q * 4) * 4);
+                            scale4(acc + ch * 8 + q * 4, z, skb + (h * 16 + ch * 8 + q * 4) * 4);
                             add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
                             add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
                             mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
@@ -636,13 +640,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             if (!was_whole) {   // a hidden key adds 0 whatever its scale holds
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
-                                    f[u] = (saw[h] >> (ch * 8 + q * 4 + u)) & 1u ? f[u] : 0.0f;
+                                    f[u] = (saw[h >> 1] >> ((h & 1) * 16 + ch * 8 + q * 4 + u)) & 1u ? f[u] : 0.0f;
                             }
                             const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
                             x[2 * q] = *reinterpret_cast<const uint32_t *>(&lo);
                             x[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&hi);
                         }
-                        const uint32_t c16 = static_cast<uint32_t>(h * 4 + ch) ^ (static_cast<uint32_t>(r) & 7u);
+                        const uint32_t c16 = static_cast<uint32_t>(h * 2 + ch) ^ (static_cast<uint32_t>(r) & 7u);
                         sts_v4(prow + b * C::P_BUF + (c16 << 4), x[0], x[1], x[2], x[3]);
                     }
                 }

@@ -44,8 +44,8 @@
  *    does an index in the caller's device memory that is out of range (SDNQ_ERR_INDEX).
  *  - Only sm_100 devices are supported (SDNQ_ERR_UNSUPPORTED otherwise). There is no CPU
  *    and no other-architecture path.
- *  - The int8 GEMMs, the attention kernel and the attention preparation are launched with
- *    programmatic stream serialization. Such a kernel may start its prologue (barriers,
+ *  - The int8 GEMMs, the attention kernels, the attention preparation and the calls on a
+ *    paged cache are launched with programmatic stream serialization. Such a kernel may start its prologue (barriers,
  *    tensor memory, descriptor prefetch) while the previous kernel in the stream drains. It
  *    reads or writes no global memory before that kernel has completed, so stream order
  *    holds for the caller's own kernels as well.
@@ -407,9 +407,10 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *   max_q: the largest number of new tokens of a sequence, or a bound on it. It chooses the
  *     kernels only; a wrong one costs time, never results.
  *   scale: finite and >= 0, usually fp32(1/sqrt(D)). window, sinks >= 0.
- *   ws: sdnq_attention_paged_workspace(H, Hkv, D) bytes, 256-byte aligned, for partial sums of
- *     one call; nothing in it needs clearing or is kept between calls. Calls that may overlap
- *     on the GPU need separate ones.
+ *   ws: sdnq_attention_paged_workspace(H, Hkv, D) bytes, 256-byte aligned (about 48 MB for
+ *     D = 128, 24 MB for D = 64, whatever the batch), for partial sums of one call; nothing in
+ *     it needs clearing or is kept between calls. Calls that may overlap on the GPU need
+ *     separate ones.
  *   out [T][H][D] bf16, token stride ldo; rows past cu_q[B] (past B without cu_q) are left as
  *     they are. out may not overlap q.
  * A page id out of range hides its keys; row offsets that decrease or leave [0, T] leave their

@@ -72,6 +72,8 @@ CASES = [
     ([280], [70], 4, 1, 64, 256, 0, 0, 256),
     ([900, 30], [17, 30], 8, 1, 128, 16, 0, 0, 128),
     ([777], [1], 20, 1, 128, 64, 300, 70, 256),
+    ([300, 77], None, 40, 1, 64, 32, 0, 0, 256),              # single tokens with more rows than the small tiles take
+    ([500], None, 300, 1, 128, 16, 100, 3, 8),
 ]
 
 
