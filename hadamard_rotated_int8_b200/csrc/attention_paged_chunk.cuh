@@ -615,41 +615,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 // P = 2^(y - m) s_v, bf16, into this buffer's swizzled K-major tile (attention.cuh)
                 const float neg_m = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0, 0, 0, 0};
+                auto weigh = [&](auto masked) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    tmem_ld_32x32b_x16(s_addr + (b ^ 1u) * 64u + h * 16u, acc);   // (of the last step: not used)
-                    tmem_ld_wait();
+                    for (int h = 0; h < 4; ++h) {
+                        tmem_ld_32x32b_x16(s_addr + (b ^ 1u) * 64u + h * 16u, acc);   // (of the last step: not used)
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int ch = 0; ch < 2; ++ch) {
-                        uint32_t x[4];
+                        for (int ch = 0; ch < 2; ++ch) {
+                            uint32_t x[4];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float *z = y + h * 16 + ch * 8 + q * 4;
-                            const float4 v4 = lds_v4(svb + (h * 16 + ch * 8 + q * 4) * 4);
-                            float f[4];
-                            fma2(f[0], f[1], z[0], z[1], row_f, row_f, neg_m, neg_m);
-                            fma2(f[2], f[3], z[2], z[3], row_f, row_f, neg_m, neg_m);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                f[u] = ex2_approx(f[u]);
-                            scale4(acc + ch * 8 + q * 4, z, skb + (h * 16 + ch * 8 + q * 4) * 4);
-                            add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
-                            add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
-                            mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
-                            mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
-                            if (!was_whole) {   // a hidden key adds 0 whatever its scale holds
+                            for (int q = 0; q < 2; ++q) {
+                                float *z = y + h * 16 + ch * 8 + q * 4;
+                                const float4 v4 = lds_v4(svb + (h * 16 + ch * 8 + q * 4) * 4);
+                                float f[4];
+                                fma2(f[0], f[1], z[0], z[1], row_f, row_f, neg_m, neg_m);
+                                fma2(f[2], f[3], z[2], z[3], row_f, row_f, neg_m, neg_m);
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
-                                    f[u] = (saw[h >> 1] >> ((h & 1) * 16 + ch * 8 + q * 4 + u)) & 1u ? f[u] : 0.0f;
+                                    f[u] = ex2_approx(f[u]);
+                                scale4(acc + ch * 8 + q * 4, z, skb + (h * 16 + ch * 8 + q * 4) * 4);
+                                add2(ls[0], ls[1], ls[0], ls[1], f[0], f[1]);
+                                add2(ls[2], ls[3], ls[2], ls[3], f[2], f[3]);
+                                mul2(f[0], f[1], f[0], f[1], v4.x, v4.y);
+                                mul2(f[2], f[3], f[2], f[3], v4.z, v4.w);
+                                if (decltype(masked)::value) {   // a hidden key adds 0 whatever its scale holds
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u)
+                                        f[u] = (saw[h >> 1] >> ((h & 1) * 16 + ch * 8 + q * 4 + u)) & 1u ? f[u] : 0.0f;
+                                }
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+                                x[2 * q] = *reinterpret_cast<const uint32_t *>(&lo);
+                                x[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&hi);
                             }
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
-                            x[2 * q] = *reinterpret_cast<const uint32_t *>(&lo);
-                            x[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&hi);
+                            const uint32_t c16 = static_cast<uint32_t>(h * 2 + ch) ^ (static_cast<uint32_t>(r) & 7u);
+                            sts_v4(prow + b * C::P_BUF + (c16 << 4), x[0], x[1], x[2], x[3]);
                         }
-                        const uint32_t c16 = static_cast<uint32_t>(h * 2 + ch) ^ (static_cast<uint32_t>(r) & 7u);
-                        sts_v4(prow + b * C::P_BUF + (c16 << 4), x[0], x[1], x[2], x[3]);
                     }
-                }
+                };
+                if (was_whole)
+                    weigh(PagedFlag<false>());
+                else
+                    weigh(PagedFlag<true>());
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
