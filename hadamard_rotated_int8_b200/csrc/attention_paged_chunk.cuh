@@ -18,7 +18,11 @@
 //   (sums rescaled only when the maximum grows by more than 8), and P = probability * s_v in
 //   bf16. At the end of a segment the rotation is undone in registers.
 // Code size matters: the roles share one instruction cache, and a loop body that overflows it
-// runs several times slower; so the loops are small, rolled where they can be.
+// runs several times slower; so the loops are small, rolled where they can be, and the masks'
+// instructions are kept off the path of wholly visible steps.
+// 2048 tokens over 16384 keys, 32 heads over 8 of 128: 590 us in this kernel, 870 TFLOP/s of
+// products, half of them int8 (floor 233 us). A step of 64 keys takes 2600 cycles; its exponentials
+// need 1024, its products 900 and its instructions about 1600 issue cycles a scheduler.
 #pragma once
 
 #include "attention_paged.cuh"
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             };
             // acc * s_k of 4 columns (converting takes one instruction an element here; adding the
             // magic number and subtracting it again, one and a half: 659 against 646 us for a chunk
-            // of 2048 over 16384 keys, 32 heads over 8)
+            // of 2048 over 16384 keys at the time, 32 heads over 8)
             auto scale4 = [&](const uint32_t *acc, float *y, uint32_t at) {
                 const float4 k4 = lds_v4(at);   // a broadcast
                 float f[4];

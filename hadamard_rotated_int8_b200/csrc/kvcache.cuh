@@ -142,7 +142,9 @@ __device__ __forceinline__ void quant_row_lanes(float (&v)[E], int32_t g, float 
 
 // A warp takes 8 consecutive (token, key or value, head) rows, four lanes a row, so that only
 // the last two stages of the butterfly need shuffles; the next rows' elements are on their way
-// during a row's arithmetic.
+// during a row's arithmetic. About 600 instructions for 8 rows of 128, issued 59% of the time:
+// 16400 tokens of 8 heads of 128 take 30 us where the bytes would take 15.5 (8 lanes a row: 32
+// us).
 constexpr int kWriteThreads = 256;
 
 template <int D>
@@ -234,7 +236,9 @@ __device__ __forceinline__ void async_copy_4(uint32_t to, const void *from, cons
 // lane the same elements of the result. The stages at distance 32 and 64 add what the lane has.
 // About 300 instructions for 2048 elements (in fp32 with shuffles: 900). What bounds it is the
 // number of rows on their way, 128 bytes each from anywhere: every warp keeps kReadStages - 1
-// tiles of 16 in flight through its own ring in shared memory.
+// tiles of 16 in flight through its own ring in shared memory. 100003 tokens of 8 heads of 128
+// take 108 us, 5.8 TB/s; writing alone (a fill of the same bytes) takes 107. With the rows of a
+// token, not of a head, side by side in a tile, and one block in four not resident: 155 us.
 constexpr int kReadThreads = 128, kReadStages = 4;
 
 template <int D>
