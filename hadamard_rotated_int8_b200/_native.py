@@ -132,6 +132,29 @@ def _stream(stream):
     return _P(int(stream))
 
 
+def _torch_stream(stream):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    # 0 and 1 (cudaStreamLegacy) both name the default stream
+    return torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+
+
+def _empty(shape, dtype, device, stream, scratch: bool = False, zeroed: bool = False):
+    """Memory for a call that runs on ``stream`` (None: the current one), taken from that stream's
+    share of torch's allocator. Memory of the current stream may still be in use there, by work
+    that ``stream`` does not wait for. An output goes back to the caller, so the allocator is told
+    that the current stream uses it too; scratch memory lives on ``stream`` alone."""
+    make = torch.zeros if zeroed else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        t = make(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _ptr(t: torch.Tensor | None):
     return _P(t.data_ptr()) if t is not None else _P(0)
 
@@ -190,11 +213,11 @@ def _dense(t: torch.Tensor, name: str):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _rows_out(M: int, N: int, dtype, device) -> torch.Tensor:
+def _rows_out(M: int, N: int, dtype, device, stream) -> torch.Tensor:
     """[M, N] output whose row stride is padded to a multiple of 8 elements (the library
     wants 16-byte aligned rows); returned as a view of the first N columns."""
     ld = (N + 7) // 8 * 8
-    buf = torch.empty((M, ld), dtype=dtype, device=device)
+    buf = _empty((M, ld), dtype, device, stream)
     return buf[:, :N] if ld != N else buf
 
 
@@ -204,8 +227,8 @@ def sdnq_rotate_quant_weight(W: torch.Tensor, group: int = 256, qW=None, sW=None
     """W [N, K] bf16 -> (qW [N, K] int8, sW [N] fp32)."""
     _req(W, torch.bfloat16, "W", 2)
     N, K = W.shape
-    qW = torch.empty((N, K), dtype=torch.int8, device=W.device) if qW is None else qW
-    sW = torch.empty((N,), dtype=torch.float32, device=W.device) if sW is None else sW
+    qW = _empty((N, K), torch.int8, W.device, stream) if qW is None else qW
+    sW = _empty((N,), torch.float32, W.device, stream) if sW is None else sW
     _mat(qW, torch.int8, N, K, "qW", dense=True)
     _vec(sW, torch.float32, N, "sW")
     _check(lib().sdnq_rotate_quant_weight(_ptr(W), N, K, W.stride(0), group, _ptr(qW), _ptr(sW),
@@ -217,8 +240,8 @@ def sdnq_rotquant_act(x: torch.Tensor, group: int = 256, qx=None, sx=None, strea
     """x [M, K] bf16 -> (qx [M, K] int8, sx [M] fp32)."""
     _req(x, torch.bfloat16, "x", 2)
     M, K = x.shape
-    qx = torch.empty((M, K), dtype=torch.int8, device=x.device) if qx is None else qx
-    sx = torch.empty((M,), dtype=torch.float32, device=x.device) if sx is None else sx
+    qx = _empty((M, K), torch.int8, x.device, stream) if qx is None else qx
+    sx = _empty((M,), torch.float32, x.device, stream) if sx is None else sx
     _mat(qx, torch.int8, M, K, "qx", dense=True)
     _vec(sx, torch.float32, M, "sx")
     _check(lib().sdnq_rotquant_act(_ptr(x), M, K, x.stride(0), group, _ptr(qx), _ptr(sx),
@@ -226,7 +249,7 @@ def sdnq_rotquant_act(x: torch.Tensor, group: int = 256, qx=None, sx=None, strea
     return qx, sx
 
 
-def _linear_operands(qx, sx, qW, sW, bias, out, acc_out, code_dtype=torch.int8,
+def _linear_operands(qx, sx, qW, sW, bias, out, acc_out, stream, code_dtype=torch.int8,
                      acc_dtype=torch.int32):
     """Checks the operands of a linear call; returns (M, N, K, out)."""
     _req(qx, code_dtype, "qx", 2)
@@ -240,7 +263,7 @@ def _linear_operands(qx, sx, qW, sW, bias, out, acc_out, code_dtype=torch.int8,
     _vec(sx, torch.float32, M, "sx")
     _vec(sW, torch.float32, N, "sW")
     _vec(bias, torch.bfloat16, N, "bias", optional=True)
-    out = _rows_out(M, N, torch.bfloat16, qx.device) if out is None else out
+    out = _rows_out(M, N, torch.bfloat16, qx.device, stream) if out is None else out
     _mat(out, torch.bfloat16, M, N, "out")
     if acc_out is not None:
         _mat(acc_out, acc_dtype, M, N, "acc_out", dense=True)
@@ -248,7 +271,7 @@ def _linear_operands(qx, sx, qW, sW, bias, out, acc_out, code_dtype=torch.int8,
 
 
 def _linear_call(name, qx, sx, qW, sW, bias, out, acc_out, stream):
-    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out)
+    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out, stream)
     _check(getattr(lib(), name)(_ptr(qx), _ptr(sx), _ptr(qW), _ptr(sW), _ptr(bias), M, N, K,
                                 _ptr(out), out.stride(0), _ptr(acc_out), _stream(stream)), name)
     return out
@@ -263,8 +286,8 @@ def sdnq_rotquant_fp8(x, group: int, q=None, s=None, stream=None):
     """Rows of x [M, K] bf16 -> (e4m3 codes uint8 [M, K], fp32 scales [M]), rotated."""
     _req(x, torch.bfloat16, "x", 2)
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device) if q is None else q
-    s = torch.empty((M,), dtype=torch.float32, device=x.device) if s is None else s
+    q = _empty((M, K), torch.uint8, x.device, stream) if q is None else q
+    s = _empty((M,), torch.float32, x.device, stream) if s is None else s
     _mat(q, torch.uint8, M, K, "q", dense=True)
     _vec(s, torch.float32, M, "s")
     _check(lib().sdnq_rotquant_fp8(_ptr(x), M, K, x.stride(0), group, _ptr(q), _ptr(s),
@@ -274,7 +297,7 @@ def sdnq_rotquant_fp8(x, group: int, q=None, s=None, stream=None):
 
 def sdnq_fp8_linear(qx, sx, qW, sW, bias=None, out=None, acc_out=None, stream=None):
     """out [M, N] bf16 from e4m3 codes qx [M, K], qW [N, K] (uint8) and their scales."""
-    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out, torch.uint8,
+    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out, stream, torch.uint8,
                                     torch.float32)
     _check(lib().sdnq_fp8_linear(_ptr(qx), _ptr(sx), _ptr(qW), _ptr(sW), _ptr(bias), M, N, K,
                                  _ptr(out), out.stride(0), _ptr(acc_out), _stream(stream)),
@@ -303,9 +326,9 @@ def sdnq_attention_int8qk(q, k, v, group: int = 256, scale: float | None = None,
     if k.shape != (B, Lk, H, D) or v.shape != k.shape:
         raise ValueError("q, k, v shapes disagree")
     total, _ = attention_workspace(B, Lq, Lk, H, D)
-    ws = torch.empty(total, dtype=torch.uint8, device=q.device) if ws is None else ws
+    ws = _empty(total, torch.uint8, q.device, stream, scratch=True) if ws is None else ws
     _vec(ws, torch.uint8, total, "ws")
-    out = torch.empty_like(q) if out is None else out
+    out = _empty(q.shape, torch.bfloat16, q.device, stream) if out is None else out
     _req(out, torch.bfloat16, "out", 4)
     _dense(out, "out")
     if out.shape != q.shape:
@@ -327,7 +350,7 @@ def sdnq_attention_prep(q, k, group: int = 256, smooth_k: bool = True, ws=None, 
     if k.shape[0] != B or k.shape[2:] != q.shape[2:]:
         raise ValueError("q and k shapes disagree")
     total, _ = attention_workspace(B, Lq, Lk, H, D)
-    ws = torch.empty(total, dtype=torch.uint8, device=q.device) if ws is None else ws
+    ws = _empty(total, torch.uint8, q.device, stream) if ws is None else ws
     _vec(ws, torch.uint8, total, "ws")
     _check(lib().sdnq_attention_prep(_ptr(q), _ptr(k), B, Lq, Lk, H, D, group,
                                      1 if smooth_k else 0, _ptr(ws), ws.numel(), _stream(stream)),
@@ -342,7 +365,7 @@ def sdnq_attention_core(v, Lq: int, ws, scale: float | None = None, out=None, st
     B, Lk, H, D = v.shape
     total, _ = attention_workspace(B, Lq, Lk, H, D)
     _vec(ws, torch.uint8, total, "ws")
-    out = torch.empty((B, Lq, H, D), dtype=torch.bfloat16, device=v.device) if out is None else out
+    out = _empty((B, Lq, H, D), torch.bfloat16, v.device, stream) if out is None else out
     _req(out, torch.bfloat16, "out", 4)
     _dense(out, "out")
     if tuple(out.shape) != (B, Lq, H, D):
@@ -360,14 +383,14 @@ def fused_sync_words(M: int) -> int:
 _SYNC_CACHE = {}
 
 
-def _sync_buffer(device, stream_handle: int, M: int):
+def _sync_buffer(device, stream, stream_handle: int, M: int):
     """A zeroed counter buffer for sdnq_int8_linear_fused, one per (device, stream); the
     kernel leaves it zero after every successful call, so it is reused as it is."""
     key = (device.index, stream_handle)
     need = fused_sync_words(M)
     buf = _SYNC_CACHE.get(key)
     if buf is None or buf.numel() < need:
-        buf = torch.zeros(max(need, 256), dtype=torch.int32, device=device)
+        buf = _empty(max(need, 256), torch.int32, device, stream, scratch=True, zeroed=True)
         _SYNC_CACHE[key] = buf
     return buf
 
@@ -389,14 +412,14 @@ def sdnq_int8_linear_fused(x, group: int, qW, sW, bias=None, qx_ws=None, sx_ws=N
     if qW.shape[1] != K:
         raise ValueError("x and qW disagree on K")
     dev = x.device
-    qx_ws = torch.empty((M, K), dtype=torch.int8, device=dev) if qx_ws is None else qx_ws
-    sx_ws = torch.empty((M,), dtype=torch.float32, device=dev) if sx_ws is None else sx_ws
-    _, _, _, out = _linear_operands(qx_ws, sx_ws, qW, sW, bias, out, acc_out)
+    qx_ws = _empty((M, K), torch.int8, dev, stream, scratch=True) if qx_ws is None else qx_ws
+    sx_ws = _empty((M,), torch.float32, dev, stream, scratch=True) if sx_ws is None else sx_ws
+    _, _, _, out = _linear_operands(qx_ws, sx_ws, qW, sW, bias, out, acc_out, stream)
     if sync_ws is not None:
         _vec(sync_ws, torch.int32, fused_sync_words(M), "sync_ws")
     st = _stream(stream)
     if sync_ws is None:
-        sync_ws = _sync_buffer(dev, st.value or 0, M)
+        sync_ws = _sync_buffer(dev, stream, st.value or 0, M)
     _check(lib().sdnq_int8_linear_fused(_ptr(x), x.stride(0), group, _ptr(qW), _ptr(sW),
                                         _ptr(bias), M, N, K, _ptr(qx_ws), _ptr(sx_ws),
                                         _ptr(sync_ws), _ptr(out), out.stride(0), _ptr(acc_out),
@@ -431,11 +454,11 @@ def sdnq_int8_linear_grad_input(dy, qW, sW, group: int, qg_ws=None, sg_ws=None, 
     K = qW.shape[1]
     dev = dy.device
     _vec(sW, torch.float32, N, "sW")
-    qg_ws = torch.empty((M, N), dtype=torch.int8, device=dev) if qg_ws is None else qg_ws
-    sg_ws = torch.empty((M,), dtype=torch.float32, device=dev) if sg_ws is None else sg_ws
+    qg_ws = _empty((M, N), torch.int8, dev, stream, scratch=True) if qg_ws is None else qg_ws
+    sg_ws = _empty((M,), torch.float32, dev, stream, scratch=True) if sg_ws is None else sg_ws
     _mat(qg_ws, torch.int8, M, N, "qg_ws", dense=True)
     _vec(sg_ws, torch.float32, M, "sg_ws")
-    out = _rows_out(M, K, torch.bfloat16, dev) if out is None else out
+    out = _rows_out(M, K, torch.bfloat16, dev, stream) if out is None else out
     _mat(out, torch.bfloat16, M, K, "out")
     if acc_out is not None:
         _mat(acc_out, torch.int32, M, K, "acc_out", dense=True)
@@ -451,8 +474,8 @@ def sdnq_quant_grad_output(dy, sW, qg=None, sg=None, stream=None):
     _req(dy, torch.bfloat16, "dy", 2)
     M, N = dy.shape
     _vec(sW, torch.float32, N, "sW")
-    qg = torch.empty((M, N), dtype=torch.int8, device=dy.device) if qg is None else qg
-    sg = torch.empty((M,), dtype=torch.float32, device=dy.device) if sg is None else sg
+    qg = _empty((M, N), torch.int8, dy.device, stream) if qg is None else qg
+    sg = _empty((M,), torch.float32, dy.device, stream) if sg is None else sg
     _mat(qg, torch.int8, M, N, "qg", dense=True)
     _vec(sg, torch.float32, M, "sg")
     _check(lib().sdnq_quant_grad_output(_ptr(dy), dy.stride(0), _ptr(sW), M, N, _ptr(qg),
@@ -471,7 +494,7 @@ def sdnq_int8_grad_input_gemm(qg, sg, qW, group: int, out=None, acc_out=None, st
         raise ValueError("qg and qW disagree on N")
     K = qW.shape[1]
     _vec(sg, torch.float32, M, "sg")
-    out = _rows_out(M, K, torch.bfloat16, qg.device) if out is None else out
+    out = _rows_out(M, K, torch.bfloat16, qg.device, stream) if out is None else out
     _mat(out, torch.bfloat16, M, K, "out")
     if acc_out is not None:
         _mat(acc_out, torch.int32, M, K, "acc_out", dense=True)
@@ -481,9 +504,9 @@ def sdnq_int8_grad_input_gemm(qg, sg, qW, group: int, out=None, acc_out=None, st
     return out
 
 
-def _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out):
+def _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out, stream):
     """Checks the operands of a LoRA linear call; returns (M, N, K, rank, out)."""
-    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out)
+    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out, stream)
     _req(x, torch.bfloat16, "x", 2)
     if tuple(x.shape) != (M, K):
         raise ValueError(f"x: expected shape {(M, K)}, got {tuple(x.shape)}")
@@ -500,8 +523,8 @@ def _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out):
 def sdnq_int8_linear_lora(qx, sx, qW, sW, bias, x, A, B, lora_scale: float = 1.0, u_ws=None,
                           out=None, acc_out=None, stream=None):
     """As sdnq_int8_linear plus lora_scale * bf16(x A) B; u_ws [M, rank] receives bf16(x A)."""
-    M, N, K, rank, out = _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out)
-    u_ws = torch.empty((M, rank), dtype=torch.bfloat16, device=qx.device) if u_ws is None else u_ws
+    M, N, K, rank, out = _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out, stream)
+    u_ws = _empty((M, rank), torch.bfloat16, qx.device, stream, scratch=True) if u_ws is None else u_ws
     _mat(u_ws, torch.bfloat16, M, rank, "u_ws", dense=True)
     _check(lib().sdnq_int8_linear_lora(_ptr(qx), _ptr(sx), _ptr(qW), _ptr(sW), _ptr(bias),
                                        _ptr(x), x.stride(0), _ptr(A), _ptr(B), rank,
@@ -521,7 +544,7 @@ def sdnq_lora_down(x, A, u=None, stream=None):
     if A.shape[0] != K:
         raise ValueError(f"A: expected {K} rows, got {A.shape[0]}")
     rank = A.shape[1]
-    u = torch.empty((M, rank), dtype=torch.bfloat16, device=x.device) if u is None else u
+    u = _empty((M, rank), torch.bfloat16, x.device, stream) if u is None else u
     _mat(u, torch.bfloat16, M, rank, "u", dense=True)
     _check(lib().sdnq_lora_down(_ptr(x), x.stride(0), _ptr(A), rank, M, K, _ptr(u),
                                 _stream(stream)), "sdnq_lora_down")
@@ -532,7 +555,7 @@ def sdnq_int8_linear_lora_up(qx, sx, qW, sW, bias, u, B, lora_scale: float = 1.0
                              acc_out=None, stream=None):
     """sdnq_int8_linear plus lora_scale * u B from a given u [M, rank] (as written by
     sdnq_lora_down); B [rank, N] bf16."""
-    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out)
+    M, N, K, out = _linear_operands(qx, sx, qW, sW, bias, out, acc_out, stream)
     _req(B, torch.bfloat16, "B", 2)
     _dense(B, "B")
     rank = B.shape[0]
@@ -554,7 +577,7 @@ def sdnq_int8_linear_lora_noalloc(qx, sx, qW, sW, bias, x, A, B, lora_scale: flo
     """sdnq_int8_linear_lora for callers that cannot provide device memory for the u
     workspace: u lives in a fixed 8 MiB array inside the library (M * rank must not exceed
     NOALLOC_MAX_U_ELEMS). Calls that overlap on the GPU share that array and race."""
-    M, N, K, rank, out = _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out)
+    M, N, K, rank, out = _lora_operands(qx, sx, qW, sW, bias, x, A, B, out, acc_out, stream)
     if M * rank > NOALLOC_MAX_U_ELEMS:
         raise ValueError(f"M * rank = {M * rank} exceeds the library's fixed scratch of "
                          f"{NOALLOC_MAX_U_ELEMS} values; use sdnq_int8_linear_lora with u_ws")
@@ -571,7 +594,7 @@ def sdnq_gelu_bf16(x: torch.Tensor, out=None, stream=None):
     """Exact-erf GELU, bf16 -> bf16 (the MLP glue between up and down projections)."""
     _req(x, torch.bfloat16, "x", 2)
     M, N = x.shape
-    out = _rows_out(M, N, torch.bfloat16, x.device) if out is None else out
+    out = _rows_out(M, N, torch.bfloat16, x.device, stream) if out is None else out
     _mat(out, torch.bfloat16, M, N, "out")
     _check(lib().sdnq_gelu_bf16(_ptr(x), M, N, x.stride(0), _ptr(out), out.stride(0),
                                 _stream(stream)), "sdnq_gelu_bf16")
@@ -646,20 +669,10 @@ def _ints(t, dtype, n: int, name: str, dev: int):
     return m
 
 
-def _used_on(stream, *tensors):
-    """Tells torch's allocator that tensors made here (on the current stream) are used on
-    ``stream``, so that their memory is not handed out again before that work is done."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        t.record_stream(stream)
-
-
 def kv_cache(pages: int, Hkv: int, page: int, D: int, device=None):
     """The two tensors of an empty paged cache: (codes [pages, Hkv, 2, page, D] int8, scales
-    [pages, Hkv, 2, page] fp32), zeroed, so that slots that were never written read as zeros."""
+    [pages, Hkv, 2, page] fp32), zeroed (on the current stream), so that slots that were never
+    written read as zeros."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     return (torch.zeros((pages, Hkv, 2, page, D), dtype=torch.int8, device=device),
             torch.zeros((pages, Hkv, 2, page), dtype=torch.float32, device=device))
@@ -691,15 +704,13 @@ def sdnq_kv_read(slots, codes, scales, group: int = 256, k=None, v=None, stream=
     T = _ints(slots, torch.int64, -1, "slots", dev)
     ldk = ldv = Hkv * D
     if k is None:
-        k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=codes.device)
-        _used_on(stream, k)
+        k = _empty((T, Hkv, D), torch.bfloat16, codes.device, stream)
     else:
         ldk = _heads(k, "k", dev)[3]
         if k.shape != (T, Hkv, D):
             raise ValueError(f"k: expected shape {(T, Hkv, D)}, got {tuple(k.shape)}")
     if v is None:
-        v = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=codes.device)
-        _used_on(stream, v)
+        v = _empty((T, Hkv, D), torch.bfloat16, codes.device, stream)
     else:
         ldv = _heads(v, "v", dev)[3]
         if v.shape != (T, Hkv, D):
@@ -753,15 +764,13 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int = 
         raise ValueError("table: rows overlap")
     total = attention_paged_workspace(H, Hkv, D)
     if ws is None:
-        ws, have = torch.empty(total, dtype=torch.uint8, device=q.device), total
-        _used_on(stream, ws)
+        ws, have = _empty(total, torch.uint8, q.device, stream, scratch=True), total
     else:
         have = _ints(ws, torch.uint8, -1, "ws", dev)
         if have < total:
             raise ValueError(f"ws: has {have} elements, needs {total}")
     if out is None:
-        out, ldo = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device), H * D
-        _used_on(stream, out)
+        out, ldo = _empty((T, H, D), torch.bfloat16, q.device, stream), H * D
     else:
         ldo = _heads(out, "out", dev)[3]
         if out.shape != q.shape:
