@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(b_full(s), 2), mbar_init(b_empty(s), 1);
         for (int t = 0; t < 2; ++t) {
             for (int b = 0; b < 2; ++b)
-                mbar_init(done(t, b), 1), mbar_init(p_full(t, b), 4);
+                mbar_init(done(t, b), 2), mbar_init(p_full(t, b), 4);
             mbar_init(q_full(t), 4);
         }
         mbar_init(drain_bar, 1);
@@ -343,6 +343,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             mma_f16(tmem_base + 256 + t * 128, pa + 2 * kk, va + 128 * kk, IDESC_PV, !pv_first || kk != 0 ? 1u : 0u);
                     }
                     tc_commit(done(t, b));
+                    // The commit speaks of the products only. This arrival (a release) hands on what the
+                    // waits above acquired: step k's scales and mask, which the softmax reads. (It cannot
+                    // stand in for an earlier iteration's commit: what iteration k waits for, P(k - 3) or
+                    // Q or "S(0) has been read", follows the softmax's wait for iteration k - 2.)
+                    mbar_arrive(done(t, b));
                 };
                 // iteration k: S(k) goes out when P(k - 3) is written (S(k - 2), its buffer's last, has
                 // been read then), just before the product of that P with V

@@ -1,0 +1,45 @@
+"""Attention over the paged cache where one step of keys differs from the next: scales, missing pages, and ranges that
+begin and end inside a step. Against the plain 64-bit implementation, with the bound derived there."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import hadamard_rotated_int8_b200 as sd
+from hadamard_rotated_int8_b200 import _build, _native
+from tests import paged_reference as ref
+from tests.test_gpu_attention_paged import call, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    oracle.build()
+    torch.cuda.init()
+    yield
+    assert sd.sdnq_device_status() == 0
+
+
+@pytest.mark.parametrize("D,page,share,new", [(128, 16, 4, [300, 5, 77]), (64, 32, 4, [300, 5, 77]),
+                                              (128, 64, 1, [600, 40, 129]), (64, 256, 9, [100, 1, 50])])
+def test_every_step_uses_its_own_scales_and_pages(D, page, share, new):
+    """Value scales that grow and shrink by powers of two from one 64 keys to the next, pages missing in a pattern with
+    a period of its own: a step that used its neighbour's would be off by whole factors."""
+    lens = [1500, 700, 900]
+    cache = ref.Cache(1, page, D, ref.pages_of(lens, page), 71)
+    for b, L in enumerate(lens):
+        for n in range(-(-L // page)):
+            at = n * page + np.arange(page)
+            cache.scales[cache.table[b, n], 0, 1] *= 2.0 ** ((at // 64 * 5) % 11 - 5)
+            cache.scales[cache.table[b, n], 0, 0] *= 2.0 ** -(at // 64 % 3)
+    for b in range(3):
+        gone = np.arange(1, cache.table.shape[1], max(2, 7 * 16 // page))
+        cache.table[b, gone[gone < -(-lens[b] // page) - 1]] = -1
+    cu = ref.offsets(new)
+    q = ref.queries(int(cu[-1]), share, D, 72)
+    out = call(q, cache.gpu(), lens, cu, max(new))
+    assert sd.sdnq_device_status() == _native.SDNQ_ERR_INDEX
+    o, size = ref.attention(q, cache.codes, cache.scales, cache.table, lens, cu, 256, D ** -0.5)
+    check(out, o, size, max(lens))
