@@ -135,17 +135,37 @@ __device__ __forceinline__ int32_t paged_qtiles(const PagedParams &p, const Page
     return rows > p.rows_min && rows <= p.rows_max ? (rows - 1) / ROWS + 1 : 0;
 }
 
-// The key tiles of TILE keys of query tile q (ROWS rows).
+// The keys that some row of query tile q (ROWS rows) sees: [low, end) and the sinks below end.
+struct PagedReach {
+    int32_t low, end;
+
+    // [j, j + n) holds one of them. (An owner of a window gives back the pages between: their
+    // table entries are not looked up.)
+    __device__ __forceinline__ bool any(const PagedParams &p, int32_t j, int32_t n) const
+    {
+        return j < end && (j + n > low || j < p.sinks);
+    }
+};
+
+template <int ROWS>
+__device__ __forceinline__ PagedReach paged_reach(const PagedParams &p, int32_t n, int32_t len, int32_t q)
+{
+    const int32_t first = by_share(p, q * ROWS), last = by_share(p, min(q * ROWS + ROWS - 1, n * p.share - 1));
+    PagedReach r;
+    r.end = max(len - n + last + 1, 0);
+    r.low = p.window > 0 ? max(0, len - n + first - p.window + 1) : 0;
+    return r;
+}
+
+// The key tiles of TILE keys of query tile q.
 template <int TILE, int ROWS>
 __device__ __forceinline__ PagedTiles paged_tiles(const PagedParams &p, int32_t n, int32_t len, int32_t q)
 {
-    const int32_t first = by_share(p, q * ROWS), last = by_share(p, min(q * ROWS + ROWS - 1, n * p.share - 1));
-    const int32_t end = max(len - n + last + 1, 0);   // keys [0, end) are in reach
-    const int32_t low = p.window > 0 ? max(0, len - n + first - p.window + 1) : 0;
+    const PagedReach r = paged_reach<ROWS>(p, n, len, q);
     PagedTiles t;
-    t.w0 = low / TILE;
-    t.ns = min((min(p.sinks, end) + TILE - 1) / TILE, t.w0);
-    t.nt = max(t.ns + (end + TILE - 1) / TILE - t.w0, 1);
+    t.w0 = r.low / TILE;
+    t.ns = min((min(p.sinks, r.end) + TILE - 1) / TILE, t.w0);
+    t.nt = max(t.ns + (r.end + TILE - 1) / TILE - t.w0, 1);
     return t;
 }
 
@@ -501,15 +521,16 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
         while (ok && n < count) {
             const int32_t tiles = static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n));
             const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
+            const PagedReach reach = paged_reach<ROWS>(p, w.s.n, w.s.len, w.q);
             // Page ids are read 32 at a time, a batch ahead of their use; entry e is box
-            // e % nbox of the piece's tile e / nbox.
+            // e % nbox of the piece's tile e / nbox. Boxes that no row sees stay out.
             auto fetch = [&](int32_t e0) {
                 const int32_t e = e0 + static_cast<int32_t>(lane);
                 const int32_t i = w.i + (e >> nbox_shift);
                 if (i >= w.i + tiles)
                     return -1;
                 const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kFewTile + ((e & (nbox - 1)) << pp_shift);
-                if (j >= w.s.len)
+                if (!reach.any(p, j, pp))
                     return -1;
                 const int32_t id = row[j >> p.page_shift];
                 if (id < 0 || id >= p.pages) {

@@ -238,15 +238,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         while (ok && n < count) {
             const int32_t steps = piece_steps(n);
             const int32_t *row = p.table + static_cast<int64_t>(w.b) * p.table_ld;
+            const PagedReach reach = paged_reach<kChunkRows>(p, w.s.n, w.s.len, w.q);
             // Page ids are read 32 at a time, a batch ahead of their use; entry e is box
-            // e % nbox of the piece's step e / nbox.
+            // e % nbox of the piece's step e / nbox. Boxes that no row sees stay out.
             auto fetch = [&](int32_t e0) {
                 const int32_t e = e0 + static_cast<int32_t>(lane);
                 const int32_t i = w.i + (e >> nbox_shift);
                 if (i >= w.i + steps)
                     return -1;
                 const int32_t j = (i < w.t.ns ? i : w.t.w0 + i - w.t.ns) * kChunkTile + ((e & (nbox - 1)) << pp_shift);
-                if (j >= w.s.len)
+                if (!reach.any(p, j, pp))
                     return -1;
                 const int32_t id = row[j >> p.page_shift];
                 if (id < 0 || id >= p.pages) {

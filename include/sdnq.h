@@ -395,8 +395,9 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *     of sequence b (none is allowed). NULL: one new token each, row b is sequence b's.
  *   lens [B] int32: tokens of the sequence in the cache, the new ones included.
  *   table [B][max_pages] int32, row stride ldt >= max_pages: page ids of the sequence's tokens
- *     in order; entries past its length are not read. max_pages * page <= 2^30. Sequences may
- *     share pages.
+ *     in order; entries of pages that hold no token which a new token of the sequence sees (past
+ *     its length, or between the sinks and the first new token's window) may name anything.
+ *     max_pages * page <= 2^30. Sequences may share pages.
  * New token i of a sequence of length L with n new tokens is at position p = L - n + i and
  * sees the keys j <= p with (window == 0 or j > p - window or j < sinks):
  *   logit_j = (qc . kc_j) * (s_q * s_k[j]) * scale, qc and s_q the codes and scale of its q
@@ -413,9 +414,9 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *     separate ones.
  *   out [T][H][D] bf16, token stride ldo; rows past cu_q[B] (past B without cu_q) are left as
  *     they are. out may not overlap q.
- * A page id out of range hides its keys; row offsets that decrease or leave [0, T] leave their
- * sequence out; a length below 0 or above max_pages * page counts as that bound. Each records
- * SDNQ_ERR_INDEX. T == 0 or B == 0 is a no-op.
+ * A page id out of range hides its keys from the new tokens that see them; row offsets that
+ * decrease or leave [0, T] leave their sequence out; a length below 0 or above max_pages * page
+ * counts as that bound. Each records SDNQ_ERR_INDEX. T == 0 or B == 0 is a no-op.
  */
 int64_t sdnq_attention_paged_workspace(int64_t H, int64_t Hkv, int64_t D);
 sdnq_status sdnq_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,

@@ -43,3 +43,43 @@ def test_every_step_uses_its_own_scales_and_pages(D, page, share, new):
     assert sd.sdnq_device_status() == _native.SDNQ_ERR_INDEX
     o, size = ref.attention(q, cache.codes, cache.scales, cache.table, lens, cu, 256, D ** -0.5)
     check(out, o, size, max(lens))
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (128, 64), (128, 256), (64, 32)])
+@pytest.mark.parametrize("window,sinks,new", [(300, 4, [1, 1, 1]), (100, 0, [3, 1, 2]), (70, 20, [1, 1, 1]),
+                                              (300, 4, [200, 40, 3]), (65, 0, [50, 140, 257]), (1, 1, [1, 90, 2])])
+def test_pages_that_no_row_sees_may_be_gone(D, page, window, sinks, new):
+    """A sliding window's owner gives back the pages between the sinks and the window; their entries name nothing."""
+    lens = [1500, 700, 601]
+    cache = ref.Cache(2, page, D, ref.pages_of(lens, page), 81)
+    table = cache.table.copy()
+    for b, L in enumerate(lens):
+        for n in range(table.shape[1]):
+            j = n * page + np.arange(page)
+            if not (((j > L - new[b] - window) & (j < L)) | (j < min(sinks, L))).any():
+                table[b, n] = (-1, -2 ** 31, cache.P, 2 ** 31 - 1)[n % 4]
+    assert (table != cache.table).any()
+    cu = ref.offsets(new)
+    q = ref.queries(int(cu[-1]), 4, D, 82)
+    gpu = cache.gpu()
+    out = call(q, (*gpu[:2], torch.from_numpy(table).cuda()), lens, cu, max(new), window=window, sinks=sinks)
+    assert sd.sdnq_device_status() == 0
+    o, size = ref.attention(q, cache.codes, cache.scales, cache.table, lens, cu, 256, D ** -0.5, window, sinks)
+    check(out, o, size, max(lens))
+
+
+@pytest.mark.parametrize("new", [[1], [60]])
+def test_a_missing_page_that_a_row_sees_is_still_reported(new):
+    lens, window, sinks = [900], 200, 20
+    cache = ref.Cache(1, 16, 128, ref.pages_of(lens, 16), 83)
+    q = ref.queries(sum(new), 4, 128, 84)
+    for gone in (0, 1, (900 - new[0] - window + 1) // 16, 899 // 16):
+        table = cache.table.copy()
+        table[0, gone] = -1
+        gpu = cache.gpu()
+        out = call(q, (*gpu[:2], torch.from_numpy(table).cuda()), lens, ref.offsets(new), max(new), window=window,
+                   sinks=sinks)
+        assert sd.sdnq_device_status() == _native.SDNQ_ERR_INDEX, gone
+        o, size = ref.attention(q, cache.codes, cache.scales, table, lens, ref.offsets(new), 256, 128 ** -0.5, window,
+                                sinks)
+        check(out, o, size, 900)
