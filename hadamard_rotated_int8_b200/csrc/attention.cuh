@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256, 4) attn_rowquant_kernel(const AttnQuantPa
             const int64_t row = row0 + rr;
             const float s_z = __fdiv_rn(amax[rr], 127.0f);
             const bool zero = !(amax[rr] > 0.0f);
-            const bool fast = s_z >= 0x1p-126f;
+            const bool fast = s_z >= kFastStep;
             const float rcp = __frcp_rn(s_z);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {

@@ -119,7 +119,7 @@ __device__ __forceinline__ void quant_row_lanes(float (&v)[E], int32_t g, float 
     const float s_z = __fdiv_rn(m, 127.0f);
     const bool zero = !(m > 0.0f);
     float s_q = s_z;
-    if (s_z < 0x1p-126f) {   // a subnormal step: the same quotients, 2^64 times as large on both sides
+    if (s_z < kFastStep) {   // a tiny step: the same quotients, with both sides 2^64 times as large
         s_q = s_z * 0x1p64f;
         const float most = s_q * 127.0f;   // (a step rounded down may leave more than 127.5 steps)
 #pragma unroll

@@ -233,8 +233,12 @@ __device__ __noinline__ uint2 quant8_exact(float z0, float z1, float z2, float z
 // the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990): with y = RN(1/s_z) and
 // q0 = RN(z * y), the residual r = z - q0 * s_z is exact in one fused multiply-add and
 // RN(q0 + r * y) = RN(z / s_z). Q is then rounded half-to-even to an integer by adding
-// 1.5 * 2^23 (|Q| <= 127.5, so the integer lands in the low mantissa bits). Needs s_z normal;
-// otherwise (a row whose scale is subnormal) the IEEE division is used.
+// 1.5 * 2^23 (|Q| <= 127.5, so the integer lands in the low mantissa bits). The residual has bits
+// down to ulp(q0) ulp(s_z), which must not fall below fp32's 2^-149: a quotient next to the
+// smallest border between two codes (1/2 here, 2^-10 for e4m3) has ulp 2^-24 (2^-34), so s_z
+// has to be 2^-102 (2^-92) at least. Rows of a smaller step take the IEEE division.
+constexpr float kFastStep = 0x1p-90f;
+
 __device__ __forceinline__ uint2 quant8(const float (&z)[8], float s_z, float rcp, bool fast)
 {
     if (!fast)  // warp-uniform: s_z is the row's scale
@@ -317,7 +321,7 @@ __device__ __forceinline__ void quant_store_chunk(const float (&v)[4][8], int8_t
                                                   int32_t c, bool ok, uint32_t lane, float s_z,
                                                   bool zero)
 {
-    const bool fast = s_z >= 0x1p-126f;
+    const bool fast = s_z >= kFastStep;
     const float rcp = __frcp_rn(s_z);
     const int32_t base = c * 1024 + static_cast<int32_t>(lane >> 3) * 256 +
                          static_cast<int32_t>(lane & 7u) * 8;
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(512) rotquant_run_kernel(const RotquantRunPara
         const bool zero = !(amax > 0.0f);
         if (row_ok && run == 0)
             p.s[row] = zero ? 0.0f : __fmul_rn(s_z, p.c_g);
-        const bool fast = s_z >= 0x1p-126f;
+        const bool fast = s_z >= kFastStep;
         const float rcp = __frcp_rn(s_z);
         int8_t *qr = p.q + (row_ok ? row : 0) * static_cast<int64_t>(p.K);
         // codes of 16 consecutive values -> one 16-byte store
