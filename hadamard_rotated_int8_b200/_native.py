@@ -735,15 +735,15 @@ def attention_paged_workspace(H: int, Hkv: int, D: int) -> int:
     return total
 
 
-def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int = 1,
+def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int | None = None,
                          group: int = 256, scale: float | None = None, window: int = 0,
                          sinks: int = 0, ws=None, out=None, stream=None):
     """Attention of the new tokens q [T, H, D] bf16 of B sequences over their pages of the cache
     (codes, scales): out [T, H, D] bf16. table [B, max_pages] int32 page ids, lens [B] int32
     tokens in the cache (the new ones included), cu_q [B + 1] int32 row offsets of the sequences
-    (None: one new token each, T == B); max_q bounds the new tokens of a sequence. Causal; with
-    ``window`` > 0 a token sees the last ``window`` keys and the first ``sinks``. ``ws``: uint8,
-    attention_paged_workspace bytes."""
+    (None: one new token each, T == B); max_q bounds the new tokens of a sequence and chooses the
+    kernels (None: 1 without cu_q, else T). Causal; with ``window`` > 0 a token sees the last
+    ``window`` keys and the first ``sinks``. ``ws``: uint8, attention_paged_workspace bytes."""
     dev = _device()
     T, H, D, ldq = _heads(q, "q", dev)
     pages, Hkv, page, Dc = _cache(codes, scales, dev)
@@ -776,6 +776,8 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int = 
         if out.shape != q.shape:
             raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(T, 1)
     _check(lib().sdnq_attention_paged(q.data_ptr(), ldq, T, H, cu, lens.data_ptr(), B, table.data_ptr(),
                                       width, ldt, codes.data_ptr(), scales.data_ptr(), pages, page, Hkv, D,
                                       int(max_q), group, scale, int(window), int(sinks), ws.data_ptr(),

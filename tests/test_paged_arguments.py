@@ -1,0 +1,47 @@
+"""What the binding of the paged cache's calls hands to the library, and what it refuses (CPU only: the library is a
+fake, CPU tensors stand in for device tensors)."""
+import pytest
+import torch
+
+import hadamard_rotated_int8_b200 as sd
+from hadamard_rotated_int8_b200 import _native
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.endswith("_workspace"):
+                return lambda *a: 4096
+            return lambda *a: seen.append((name, a)) or 0
+
+    monkeypatch.setattr(_native, "lib", lambda: Library())
+    monkeypatch.setattr(_native, "_on_current_device", lambda t, name: None)
+    monkeypatch.setattr(_native, "_paged_ws_bytes", {})
+    monkeypatch.setattr(_native, "_stream_on", lambda stream, dev: 0)
+    return seen
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+CODES, SCALES = torch.zeros(3, 2, 2, 16, 64, dtype=torch.int8), torch.zeros(3, 2, 2, 16)
+MAX_Q = 16   # its place among the library call's arguments
+
+
+@pytest.mark.parametrize("T,cu,given,want", [(3, False, None, 1), (300, True, None, 300), (0, True, None, 1),
+                                             (300, True, 7, 7), (300, True, 1, 1), (3, False, 5, 5)])
+def test_the_bound_on_new_tokens(calls, T, cu, given, want):
+    """A caller who gives offsets and no bound has chunks of up to T tokens, not single ones."""
+    sd.sdnq_attention_paged(bf(T, 4, 64), CODES, SCALES, i32(3, 7), i32(3), cu_q=i32(4) if cu else None,
+                            **({} if given is None else {"max_q": given}))
+    (name, args), = calls
+    assert name == "sdnq_attention_paged" and args[MAX_Q] == want
+    assert args[2] == T and args[6] == 3 and args[15] == 64   # T, B and D, to keep the place honest
