@@ -210,8 +210,9 @@ sdnq_status launch_paged(PagedParams p, const DeviceInfo &dev, int64_t max_q, ui
     return launch_chunk<D>(p, dev, sms, cs);
 }
 
-// Largest context, window and sink count that the kernels' 32-bit positions hold.
-constexpr int64_t kPagedMaxKeys = 1ll << 30;
+// Largest context, window and sink count that the kernels' 32-bit positions hold; most sequences
+// (they are counted in groups of 32).
+constexpr int64_t kPagedMaxKeys = 1ll << 30, kPagedMaxSeqs = INT32_MAX - 31;
 
 sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64_t H,
                                 const int32_t *cu_q, const int32_t *lens, int64_t B,
@@ -224,7 +225,7 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     const bool work = T != 0 && B != 0;
     if (work && (!q || !lens || !table || !codes || !scales || !ws || !out))
         return SDNQ_ERR_NULL;
-    if (T < 0 || B < 0 || T > INT32_MAX || B >= INT32_MAX || H < 1 || H > 65536 || max_q < 1 ||
+    if (T < 0 || B < 0 || T > INT32_MAX || B > kPagedMaxSeqs || H < 1 || H > 65536 || max_q < 1 ||
         window < 0 || sinks < 0 || max_pages < 0 || ldt < max_pages)
         return SDNQ_ERR_SHAPE;
     sdnq_status st = validate_cache(codes, scales, pages, page, Hkv, D, group);

@@ -393,7 +393,7 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *     multiple of Hkv, query head h reads kv head h / (H / Hkv); T * H < 2^31.
  *   cu_q [B + 1] int32, not decreasing: rows cu_q[b] .. cu_q[b+1] - 1 of q are the new tokens
  *     of sequence b (none is allowed). NULL: one new token each, row b is sequence b's.
- *   lens [B] int32: tokens of the sequence in the cache, the new ones included.
+ *   lens [B] int32: tokens of the sequence in the cache, the new ones included. B <= 2^31 - 32.
  *   table [B][max_pages] int32, row stride ldt >= max_pages: page ids of the sequence's tokens
  *     in order; entries of pages that hold no token which a new token of the sequence sees (past
  *     its length, or between the sinks and the first new token's window) may name anything.

@@ -45,3 +45,19 @@ def test_the_bound_on_new_tokens(calls, T, cu, given, want):
     (name, args), = calls
     assert name == "sdnq_attention_paged" and args[MAX_Q] == want
     assert args[2] == T and args[6] == 3 and args[15] == 64   # T, B and D, to keep the place honest
+
+
+def test_more_sequences_than_the_kernels_count_are_refused():
+    """The kernels count sequences in groups of 32, in 32 bits. Fake addresses: validation comes first."""
+    from hadamard_rotated_int8_b200 import _build
+    _build.build()
+    A = 0x10000
+
+    def attn(B):
+        return _native.ctypes.CDLL(_build.LIB).sdnq_attention_paged(
+            *[t(v) for t, v in zip(_native.SIGNATURES["sdnq_attention_paged"],
+                                   (A, 512, 4, 4, A, A, B, A, 1, 1, A, A, 9, 16, 2, 128, 1, 256, 0.1, 0, 0, A, 1 << 40,
+                                    A, 512, 0))])
+
+    for B in ((1 << 31) - 31, (1 << 31) - 2):
+        assert attn(B) == _native.SDNQ_ERR_SHAPE
