@@ -747,7 +747,7 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int | 
     dev = _device()
     T, H, D, ldq = _heads(q, "q", dev)
     pages, Hkv, page, Dc = _cache(codes, scales, dev)
-    if D != Dc or H % Hkv:
+    if D != Dc or Hkv == 0 or H % Hkv:
         raise ValueError(f"q: {H} heads of {D} do not fit a cache of {Hkv} heads of {Dc}")
     if not (_is(table, torch.int32, 2, dev) and table.stride(1) == 1):
         _req(table, torch.int32, "table", 2)

@@ -223,7 +223,7 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
                                 uint16_t *out, int64_t ldo, void *stream)
 {
     const bool work = T != 0 && B != 0;
-    if (work && (!q || !lens || !table || !codes || !scales || !ws || !out))
+    if (work && (!q || !lens || (!table && max_pages != 0) || !codes || !scales || !ws || !out))
         return SDNQ_ERR_NULL;
     if (T < 0 || B < 0 || T > INT32_MAX || B > kPagedMaxSeqs || H < 1 || H > 65536 || max_q < 1 ||
         window < 0 || sinks < 0 || max_pages < 0 || ldt < max_pages)

@@ -397,7 +397,8 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *   table [B][max_pages] int32, row stride ldt >= max_pages: page ids of the sequence's tokens
  *     in order; entries of pages that hold no token which a new token of the sequence sees (past
  *     its length, or between the sinks and the first new token's window) may name anything.
- *     max_pages * page <= 2^30. Sequences may share pages.
+ *     max_pages * page <= 2^30; max_pages == 0 (no sequence has a page; table may be NULL) gives
+ *     zeros. Sequences may share pages.
  * New token i of a sequence of length L with n new tokens is at position p = L - n + i and
  * sees the keys j <= p with (window == 0 or j > p - window or j < sinks):
  *   logit_j = (qc . kc_j) * (s_q * s_k[j]) * scale, qc and s_q the codes and scale of its q

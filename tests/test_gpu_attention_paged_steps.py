@@ -83,3 +83,14 @@ def test_a_missing_page_that_a_row_sees_is_still_reported(new):
         o, size = ref.attention(q, cache.codes, cache.scales, table, lens, ref.offsets(new), 256, 128 ** -0.5, window,
                                 sinks)
         check(out, o, size, 900)
+
+
+@pytest.mark.parametrize("new", [None, [1, 40, 2]])
+def test_sequences_without_pages(new):
+    """A table without columns: no key to see, rows of zeros."""
+    cache = ref.Cache(2, 16, 128, [1], 91)
+    c, s, _ = cache.gpu()
+    cu = ref.offsets(new or [1, 1, 1])
+    q = ref.queries(int(cu[-1]), 4, 128, 92)
+    out = call(q, (c, s, torch.empty((3, 0), dtype=torch.int32, device="cuda")), [0, 0, 0], new and cu, max(new or [1]))
+    assert sd.sdnq_device_status() == 0 and not out.any()

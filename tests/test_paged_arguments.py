@@ -61,3 +61,23 @@ def test_more_sequences_than_the_kernels_count_are_refused():
 
     for B in ((1 << 31) - 31, (1 << 31) - 2):
         assert attn(B) == _native.SDNQ_ERR_SHAPE
+
+
+def test_a_cache_without_heads_is_refused(calls):
+    with pytest.raises(ValueError):
+        sd.sdnq_attention_paged(bf(3, 4, 64), CODES[:, :0], SCALES[:, :0], i32(3, 7), i32(3))
+    assert not calls
+
+
+def test_a_table_without_columns_reaches_the_library():
+    """Sequences that have no page yet: an empty tensor has no address. (Refused here for its workspace, behind the
+    check of the pointers.)"""
+    from hadamard_rotated_int8_b200 import _build
+    _build.build()
+    A = 0x10000
+    args = [A, 512, 4, 4, A, A, 3, 0, 0, 0, A, A, 9, 16, 2, 128, 1, 256, 0.1, 0, 0, A, 100, A, 512, 0]
+    fn = _native.ctypes.CDLL(_build.LIB).sdnq_attention_paged
+    types = _native.SIGNATURES["sdnq_attention_paged"]
+    assert fn(*[t(v) for t, v in zip(types, args)]) == _native.SDNQ_ERR_SHAPE
+    args[8] = args[9] = 1
+    assert fn(*[t(v) for t, v in zip(types, args)]) == _native.SDNQ_ERR_NULL
