@@ -95,35 +95,6 @@ __device__ __forceinline__ void thread_butterfly(float (&v)[D], int32_t g)
         }
 }
 
-// Waits for a phase in a handful of instructions (the loops of this kernel's roles share one
-// instruction cache, and mbar_wait_bounded's clock costs six times the code). Gives up after
-// kWaitTries tries, about 2 s (the hardware suspends the thread for 4 us each): then it raises
-// `abort` and the device error word and returns false.
-constexpr uint32_t kWaitTries = 1u << 19;
-__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity, volatile int *abort)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, %3;\n\t"
-        "AGAIN:\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
-        "@q bra AGAIN;\n\t"
-        "DONE:\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "n"(kWaitTries)
-        : "memory");
-    if (done == 0u) {
-        *abort = 1;
-        atomicOr(&g_device_error, kDevTimeout);
-    }
-    return done != 0u;
-}
-
 // True in one lane of the warp (all lanes call it).
 __device__ __forceinline__ bool elect_one()
 {

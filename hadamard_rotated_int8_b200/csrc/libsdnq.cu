@@ -1170,8 +1170,9 @@ __global__ void wait_timeout_selftest_kernel(uint64_t limit_ns)
         abort_flag = 0;
         mbar_init(smem_u32(&bar), 1);
         fence_mbar_init();
-        // nothing ever arrives: phase 0 never completes, the bounded wait gives up
+        // nothing ever arrives: phase 0 never completes, both bounded waits give up, one after the other
         mbar_wait_bounded(smem_u32(&bar), 0u, &abort_flag, limit_ns);
+        mbar_wait_tries(smem_u32(&bar), 0u, &abort_flag, static_cast<uint32_t>(limit_ns / kTryNs) + 1u);
         mbar_arrive(smem_u32(&bar));  // leave the barrier consistent
     }
 }

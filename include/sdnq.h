@@ -446,10 +446,10 @@ sdnq_status sdnq_gelu_bf16(const uint16_t *in, int64_t M, int64_t N, int64_t ld_
 sdnq_status sdnq_device_status(void *stream);
 
 /*
- * Self-test of the bounded-wait machinery: launches one small kernel whose wait can never
- * be satisfied (an mbarrier that nothing arrives on), with a limit of `limit_ns`
- * nanoseconds (1e3..1e10). The kernel gives up, records SDNQ_ERR_TIMEOUT in the device
- * error word and returns; no fault, trap or hang is involved.
+ * Self-test of the bounded-wait machinery: launches one small kernel whose two waits can
+ * never be satisfied (an mbarrier that nothing arrives on), each limited to `limit_ns`
+ * nanoseconds (1e3..1e10), the second by a number of tries of 4 us. The kernel gives up on both, records SDNQ_ERR_TIMEOUT in the device error word and
+ * returns; no fault, trap or hang is involved.
  */
 sdnq_status sdnq_selftest_wait_timeout(int64_t limit_ns, void *stream);
 
