@@ -876,6 +876,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
             few_sync();
         }
         const bool begins = w.i == 0, ends = w.i + tiles == w.t.nt;
+        const bool good = ok && *abort == 0;   // no role gave up waiting
         float *ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
 #pragma unroll 1
         for (int32_t lr = static_cast<int32_t>(warp); lr < rows; lr += 4) {
@@ -893,14 +894,14 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                 v[i] = obuf[lr * C::O_LD + lane * E + i];
             const int32_t r = r0 + lr, tok = by_share(p, r);
             if (begins && ends) {
-                if (ok)
+                if (good)
                     paged_store_row<D>(p, v, ll, w.s.q0 + tok, head0 + r - tok * p.share, lane);
             } else {
 #pragma unroll
                 for (int d = 0; d < E; ++d)
                     ws[lr * D + lane * E + d] = v[d];
                 if (lane == 0)
-                    *reinterpret_cast<float2 *>(ws + ROWS * D + 2 * lr) = make_float2(mm, ll);
+                    *reinterpret_cast<float2 *>(ws + ROWS * D + 2 * lr) = make_float2(mm, good ? ll : nanf(""));
             }
         }
         if (threadIdx.x == 0 && begins && !ends) {

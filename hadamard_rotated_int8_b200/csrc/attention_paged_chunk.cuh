@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t all_boxes = (1u << nbox) - 1u;
     auto piece_steps = [&](int64_t n) { return static_cast<int32_t>(min(static_cast<int64_t>(w.t.nt - w.i), count - n)); };
     auto piece_rows = [&] { return min(kChunkRows, w.s.n * p.share - w.q * kChunkRows); };
-    // A role that gave up waiting runs its loops to their end without waiting or storing (the
-    // loader stops loading).
+    // A role that gave up waiting raises `abort` and runs its loops to their end without waiting (the
+    // loader stops loading); from then on no output row is stored, and pieces are marked as lost.
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok && !mbar_try_wait(bar, parity))
@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             next_done((g + 1u) & 1u);
             next_done(g & 1u);
             tc_fence_after_sync();
+            const bool good = ok && *abort == 0;
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
             const bool join = finish && p.group == D;
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
                 if (finish) {
                     thread_butterfly<D / 2>(v, p.group);
-                    if (ok && lr < rows) {
+                    if (good && lr < rows) {
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e) {
                             uint32_t x[4];
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             tc_fence_before_sync();
             if (!finish && lr < rows)
-                *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, l_sum);
+                *reinterpret_cast<float2 *>(ws + kChunkRows * D + 2 * lr) = make_float2(m_used, good ? l_sum : nanf(""));
             n += steps;
             if (threadIdx.x == 128 && begins && !ends) {
                 // the segment's last step is nt - steps further on: that many blocks hold pieces
