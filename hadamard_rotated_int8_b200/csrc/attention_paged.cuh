@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                                 pr[c] = x * sv;
                                 // a hidden key adds 0 whatever its scale holds
                                 if (decltype(masked)::value)
-                                    pr[c] = x == 0.0f ? 0.0f : pr[c];
+                                    pr[c] = y[nb][kb][c] == -INFINITY ? 0.0f : pr[c];
                             }
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
                             pb[nb][kb] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h2));
@@ -892,6 +892,8 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
 #pragma unroll
             for (int i = 0; i < E; ++i)
                 v[i] = obuf[lr * C::O_LD + lane * E + i];
+            if (qs[lr] != qs[lr] && ll > 0.0f)   // a query row that is not finite, where it sees a key
+                ll = nanf("");
             const int32_t r = r0 + lr, tok = by_share(p, r);
             if (begins && ends) {
                 if (good)

@@ -651,6 +651,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             next_done(g & 1u);
             tc_fence_after_sync();
             const bool good = ok && *abort == 0;
+            if (qs[lr] != qs[lr] && l_sum > 0.0f)   // a query row that is not finite, where it sees a key
+                l_sum = nanf("");
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
             const bool join = finish && p.group == D;

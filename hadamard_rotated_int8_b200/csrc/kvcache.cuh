@@ -9,6 +9,8 @@
 // write: z = butterfly of the row over groups of G = min(group, D), s_z = fp32(amax / 127),
 //        code = clamp(rne(fp32(z / s_z))), stored scale s = fp32(s_z * c), c = fp32(1/sqrt(G)):
 //        the row quantizer of the linear path, so that z * c ~= s * code.
+//        A row whose rotation is not finite (NaN, infinities, sums past fp32's range): codes 0 and
+//        a NaN as its scale, so that what is made of it is NaN and not a plausible number.
 // read:  x = bf16(butterfly(code) * fp32(s * c)); the butterfly of whole numbers is exact in
 //        fp32 (|sum| <= 128 * 128).
 //
@@ -77,6 +79,20 @@ __device__ __forceinline__ int64_t kv_held(const KvParams &p, const KvRow &k, in
     return -1;
 }
 
+// The larger one, or NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max3_abs_nan(float m, float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return d;
+}
+
 // One row on LANES neighbouring lanes, E consecutive elements each, rotated over groups of g (a
 // run-time power of two from 8 to E LANES) and quantized: the row quantizer's adds, divisions
 // and roundings. Returns the codes, packed, and the row's stored scale.
@@ -111,13 +127,13 @@ __device__ __forceinline__ void quant_row_lanes(float (&v)[E], int32_t g, float 
         }
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-        m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < E; i += 2)
+        m = max3_abs_nan(m, v[i], v[i + 1]);
 #pragma unroll
     for (int x = 1; x < LANES; x <<= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float s_z = __fdiv_rn(m, 127.0f);
-    const bool zero = !(m > 0.0f);
+    const bool codes_0 = !(m > 0.0f && m < INFINITY);
     float s_q = s_z;
     if (s_z < kFastStep) {   // a tiny step: the same quotients, with both sides 2^64 times as large
         s_q = s_z * 0x1p64f;
@@ -134,10 +150,10 @@ __device__ __forceinline__ void quant_row_lanes(float (&v)[E], int32_t g, float 
         for (int i = 0; i < 8; ++i)
             z[i] = v[8 * c + i];
         const uint2 w = quant8(z, s_q, rcp, true);
-        codes[2 * c] = zero ? 0u : w.x;
-        codes[2 * c + 1] = zero ? 0u : w.y;
+        codes[2 * c] = codes_0 ? 0u : w.x;
+        codes[2 * c + 1] = codes_0 ? 0u : w.y;
     }
-    s = zero ? 0.0f : __fmul_rn(s_z, c_g);
+    s = !codes_0 ? __fmul_rn(s_z, c_g) : m == 0.0f ? 0.0f : nanf("");
 }
 
 // A warp takes 8 consecutive (token, key or value, head) rows, four lanes a row, so that only

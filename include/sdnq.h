@@ -368,7 +368,8 @@ sdnq_status sdnq_attention_core(const uint16_t *v, int64_t B, int64_t Lq, int64_
  *   slots [T] int64. A negative slot leaves its token out; a slot past the pool does too, and
  *   records SDNQ_ERR_INDEX. Slots that are not negative are distinct within a call: of two
  *   tokens with one slot, which one's codes (or a mix) it holds afterwards is unspecified.
- *   Rows with infinities or NaN: the codes and the scale are unspecified.
+ *   A row whose rotation is not finite (NaN, infinities, sums past fp32's range) is stored as
+ *   codes 0 with a NaN scale: it reads as NaN, and so do the attention's rows that see it.
  *
  * sdnq_kv_read: the rows of T slots as bf16, x = bf16(butterfly(code) * fp32(s * c)) with
  *   c = fp32(1/sqrt(min(group, D))). k, v [T][Hkv][D] out, strides as above. A negative slot
@@ -404,8 +405,9 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *   logit_j = (qc . kc_j) * (s_q * s_k[j]) * scale, qc and s_q the codes and scale of its q
  *   row as sdnq_kv_write makes them; o = butterfly(sum_j softmax(logit)_j * s_v[j] * vc_j) * c.
  *   Probabilities times s_v are rounded to bf16 for the product with vc (fp32 accumulation),
- *   o is rounded to bf16. A row that sees no key gives zeros. What lies in slots a row does
- *   not see (uninitialised codes, infinite or NaN scales) has no effect on it.
+ *   o is rounded to bf16. A row that sees no key gives zeros; one whose query is not finite (as
+ *   for sdnq_kv_write) gives NaN where it sees a key. What lies in slots a row does not see
+ *   (uninitialised codes, infinite or NaN scales) has no effect on it.
  *   max_q: the largest number of new tokens of a sequence, or a bound on it. It chooses the
  *     kernels only; a wrong one costs time, never results.
  *   scale: finite and >= 0, usually fp32(1/sqrt(D)). window, sinks >= 0.
