@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t s_addr = tmem_base + ((quad * 32u) << 16) + tile * 128u;
         const uint32_t o_addr = s_addr + 256u;
         const uint32_t prow = base + C::P_OFF + tile * 2u * C::P_BUF + static_cast<uint32_t>(r) * 128u;
-        uint32_t g = 0, parity = 0;   // steps of this tile; bit b: parity of the next phase of done(tile, b)
+        uint32_t g = 0, parity = 0;   // steps of this tile; bit b: parity of the next phase of done(tile, b);
+                                      // bit 2: this thread's query row is not finite
         bool open = false;
         int64_t n = 0;
         while (n < count) {
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             __syncwarp();
             // logit * log2 e = (acc * s_k) * row_f; the floor keeps 0 * -inf out
             const float row_f = fmaxf(qs[lr] * p.scale * 1.4426950408889634f, 0x1p-126f);
+            parity = qs[lr] != qs[lr] ? parity | 4u : parity & 3u;
             if (lane == 0)
                 mbar_arrive(q_full(tile));
             float m_used = -INFINITY, l_sum = 0.0f;
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             next_done(g & 1u);
             tc_fence_after_sync();
             const bool good = ok && *abort == 0;
-            if (qs[lr] != qs[lr] && l_sum > 0.0f)   // a query row that is not finite, where it sees a key
+            if ((parity & 4u) && l_sum > 0.0f)   // (asking qs again here costs the loop above 2% of its time)
                 l_sum = nanf("");
             // O, half a row at a time. A whole segment's is un-rotated: the last stage of a group of
             // D joins the halves, first, and each half has its own stages after that.
