@@ -177,6 +177,8 @@ struct PagedWalk {
     PagedTiles t;
 };
 
+// (Not to be called behind the last piece of a block: it looks at sequences one by one, and those
+// that follow may all be the other kernel's.)
 template <int TILE, int ROWS>
 __device__ __forceinline__ void walk_next_segment(const PagedParams &p, PagedWalk &w)
 {
@@ -582,7 +584,8 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                 if (++st == NST)
                     st = 0, phase ^= 1u;
             }
-            walk_next_segment<kFewTile, ROWS>(p, w);
+            if (n < count)
+                walk_next_segment<kFewTile, ROWS>(p, w);
         }
         // every copy has landed before the block may end (its consumers may have given up)
         if (lane == 0) {
@@ -916,7 +919,8 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
             desc->r0 = r0;
             piece_no = 1;
         }
-        walk_next_segment<kFewTile, ROWS>(p, w);
+        if (n < count)
+            walk_next_segment<kFewTile, ROWS>(p, w);
         few_sync();   // obuf, ml and the query codes are free again
     }
     if (threadIdx.x == 0 && piece_no == 0)

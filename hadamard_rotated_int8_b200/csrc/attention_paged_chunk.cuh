@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     vs = 0, vph ^= 1u;
             }
             n += steps;
-            walk_next_segment<kChunkTile, kChunkRows>(p, w);
+            if (n < count)
+                walk_next_segment<kChunkTile, kChunkRows>(p, w);
         }
         // every copy has landed before the block may end
         ok = true;
@@ -361,7 +362,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 g0 += static_cast<uint32_t>(steps);
                 g1 += two ? static_cast<uint32_t>(steps) : 0u;
                 n += steps;
-                walk_next_segment<kChunkTile, kChunkRows>(p, w);
+                if (n < count)
+                    walk_next_segment<kChunkTile, kChunkRows>(p, w);
             }
             tc_commit(drain_bar);
             mbar_wait_tries(drain_bar, 0u, abort);
@@ -422,7 +424,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint32_t n0 = static_cast<uint32_t>(n);
             if (static_cast<int32_t>(tile) * 128 >= rows) {   // no row in this tile
                 n += steps;
-                walk_next_segment<kChunkTile, kChunkRows>(p, w);
+                if (n < count)
+                    walk_next_segment<kChunkTile, kChunkRows>(p, w);
                 continue;
             }
             const int32_t tok = by_share(p, r0 + min(lr, rows - 1));
@@ -712,7 +715,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 desc->r0 = r0;
                 open = true;
             }
-            walk_next_segment<kChunkTile, kChunkRows>(p, w);
+            if (n < count)
+                walk_next_segment<kChunkTile, kChunkRows>(p, w);
         }
         if (threadIdx.x == 128 && !open)
             desc->pieces = 0;

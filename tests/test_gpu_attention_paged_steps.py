@@ -94,3 +94,27 @@ def test_sequences_without_pages(new):
     q = ref.queries(int(cu[-1]), 4, 128, 92)
     out = call(q, (c, s, torch.empty((3, 0), dtype=torch.int32, device="cuda")), [0, 0, 0], new and cu, max(new or [1]))
     assert sd.sdnq_device_status() == 0 and not out.any()
+
+
+def test_sequences_behind_a_blocks_last_piece_cost_nothing():
+    """A chunk in front of 40000 sequences without new tokens takes what it takes behind them: the blocks that have its
+    last pieces do not look at those sequences one by one."""
+    E, times = 40000, []
+    cache = ref.Cache(1, 16, 128, ref.pages_of([600], 16), 95)
+    c, s, t = cache.gpu()
+    q = ref.queries(300, 4, 128, 96).cuda()
+    for at in (0, E):
+        new, lens = np.zeros(E + 1, np.int64), np.zeros(E + 1, np.int32)
+        new[at], lens[at] = 300, 600
+        args = (q, c, s, t.expand(E + 1, -1).contiguous(), torch.from_numpy(lens).cuda())
+        cu = torch.from_numpy(ref.offsets(new)).cuda()
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        for e in (begin, end):      # the second call is the timed one
+            begin.record()
+            out = sd.sdnq_attention_paged(*args, cu_q=cu)
+            e.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end))
+        o, size = ref.attention(q[-1:].cpu(), cache.codes, cache.scales, cache.table, [600], [0, 1], 256, 128 ** -0.5)
+        check(out[-1:], o, size, 600)
+    assert times[0] < 3 * times[1], times
