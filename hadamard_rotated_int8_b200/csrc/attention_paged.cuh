@@ -769,10 +769,14 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                         }
                     }
                 }
-                uint32_t pb[NB][4];   // probabilities times s_v: keys PI(2t), PI(2t + 1), query row g
-                auto weigh = [&](auto masked) {
+                // probabilities times s_v: keys PI(2t), PI(2t + 1), query row g; what their rounding to bf16
+                // leaves is a second operand of the same products. So o keeps 16 bits of them: its error is
+                // that of its own rounding (relative to 64 bits 0.00165 where one operand gives 0.00225; 64
+                // sequences of up to 8192 keys take 105 instead of 102 us)
+                uint32_t pb[NB][2], pl[NB][2];
+                auto weigh = [&](auto masked, int kk) {
 #pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
+                    for (int kb = 2 * kk; kb < 2 * kk + 2; ++kb) {
                         const float sv = lds_f(sc + (my_row[kb >> 1] + 8u * (kb & 1) + pp + krow_n) * 4u);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
@@ -788,17 +792,21 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                                     pr[c] = y[nb][kb][c] == -INFINITY ? 0.0f : pr[c];
                             }
                             const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
-                            pb[nb][kb] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h2));
+                            const uint32_t hi = *reinterpret_cast<const uint32_t *>(&h2);
+                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(pr[0] - __uint_as_float(hi << 16),
+                                                                            pr[1] - __uint_as_float(hi & 0xffff0000u));
+                            pb[nb][kb & 1] = movmatrix_trans(hi);
+                            pl[nb][kb & 1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&l2));
                         }
                     }
                 };
-                if (whole)
-                    weigh(PagedFlag<false>());
-                else
-                    weigh(PagedFlag<true>());
                 // values of keys PI(2t), PI(2t + 1) of two 8-key blocks, this lane's D / 8 dims
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
+                    if (whole)
+                        weigh(PagedFlag<false>(), kk);
+                    else
+                        weigh(PagedFlag<true>(), kk);
                     uint32_t vb[4][D / 32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -820,8 +828,10 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                         for (int i = 0; i < 4; ++i)
                             a[i] = codes_to_bf16x2(vb[i & 2][j >> 1], vb[(i & 2) + 1][j >> 1], (2 * j + (i & 1)) & 3);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pb[nb][2 * kk], pb[nb][2 * kk + 1]);
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pb[nb][0], pb[nb][1]);
+                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+                        }
                     }
                 }
             }

@@ -404,12 +404,14 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  * sees the keys j <= p with (window == 0 or j > p - window or j < sinks):
  *   logit_j = (qc . kc_j) * (s_q * s_k[j]) * scale, qc and s_q the codes and scale of its q
  *   row as sdnq_kv_write makes them; o = butterfly(sum_j softmax(logit)_j * s_v[j] * vc_j) * c.
- *   Probabilities times s_v are rounded to bf16 for the product with vc (fp32 accumulation),
- *   o is rounded to bf16. A row that sees no key gives zeros; one whose query is not finite (as
- *   for sdnq_kv_write) gives NaN where it sees a key. What lies in slots a row does not see
- *   (uninitialised codes, infinite or NaN scales) has no effect on it.
+ *   Maxima, sums and accumulators are fp32, o is rounded to bf16. Probabilities times s_v enter
+ *   the product with vc as two bf16 numbers (16 bits), or rounded to one for sequences of more
+ *   than 32 query rows (new tokens times H / Hkv) a kv head where max_q allows as many.
+ *   A row that sees no key gives zeros; one whose query is not finite (as for sdnq_kv_write)
+ *   gives NaN where it sees a key. What lies in slots a row does not see (uninitialised codes,
+ *   infinite or NaN scales) has no effect on it.
  *   max_q: the largest number of new tokens of a sequence, or a bound on it. It chooses the
- *     kernels only; a wrong one costs time, never results.
+ *     kernels only; a wrong one costs time, and changes results by no more than that rounding.
  *   scale: finite and >= 0, usually fp32(1/sqrt(D)). window, sinks >= 0.
  *   ws: sdnq_attention_paged_workspace(H, Hkv, D) bytes, 256-byte aligned (about 48 MB for
  *     D = 128, 24 MB for D = 64, whatever the batch), for partial sums of one call; nothing in

@@ -118,3 +118,23 @@ def test_sequences_behind_a_blocks_last_piece_cost_nothing():
         o, size = ref.attention(q[-1:].cpu(), cache.codes, cache.scales, cache.table, [600], [0, 1], 256, 128 ** -0.5)
         check(out[-1:], o, size, 600)
     assert times[0] < 3 * times[1], times
+
+
+@pytest.mark.parametrize("lens,new,share,Hkv,D,page,window,sinks", [
+    ([300, 1, 77, 1000], None, 4, 2, 128, 16, 0, 0), ([513, 40], None, 8, 1, 64, 32, 0, 0),
+    ([900, 250], [4, 3], 4, 2, 128, 64, 0, 0), ([700, 300], [2, 4], 6, 1, 64, 16, 90, 4),
+    ([9000], None, 3, 1, 128, 64, 0, 0), ([1500, 333], None, 20, 1, 128, 16, 200, 1)])
+def test_few_rows_are_as_exact_as_their_output(lens, new, share, Hkv, D, page, window, sinks):
+    """Up to 32 query rows a kv head: every element within its own rounding to bf16 (half a step) and what 16 bits of
+    the probabilities (2^-17 each) and the fp32 sums leave; the 2-norm of a row bounds its elements."""
+    cache = ref.Cache(Hkv, page, D, ref.pages_of(lens, page), 97)
+    cu = ref.offsets(new or [1] * len(lens))
+    q = ref.queries(int(cu[-1]), share * Hkv, D, 98)
+    out = call(q, cache.gpu(), lens, None if new is None else cu, max(new or [1]), window=window, sinks=sinks)
+    o, size = ref.attention(q, cache.codes, cache.scales, cache.table, lens, cu, 256, D ** -0.5, window, sinks)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(o), 2.0 ** -126))) - 7)
+    # fp32 sums over the keys, logits up to 64 a few roundings off, the exponential's 2^-22, the butterfly
+    rel = 2.0 ** -17 + 2 * max(lens) * 2.0 ** -24 + 4 * 64 * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -20
+    err = np.abs(out.float().cpu().numpy().astype(np.float64) - o)
+    lim = 0.5 * step + rel * size[..., None] * (1 + 2.0 ** -7)
+    assert np.all(err <= lim), float((err / lim).max())
