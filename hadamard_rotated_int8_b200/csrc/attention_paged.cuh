@@ -10,6 +10,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "attention.cuh"
 #include "device.cuh"
 #include "kvcache.cuh"
@@ -28,7 +30,7 @@ struct PagedParams {
     const int8_t *codes;
     const float *scales;
     int64_t pages;
-    int32_t T, B, H, Hkv;
+    int32_t T, B, Hkv;
     int32_t share;           // H / Hkv
     uint32_t share_mul, share_shift;   // n / share = n * share_mul >> share_shift for 0 <= n < 2^31
     int32_t page_shift;
@@ -439,11 +441,6 @@ __device__ __forceinline__ float lds_f(uint32_t addr)
     return v;
 }
 
-template <bool V>
-struct PagedFlag {
-    static constexpr bool value = V;
-};
-
 // Barrier of the four warps that compute.
 __device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -804,9 +801,9 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     if (whole)
-                        weigh(PagedFlag<false>(), kk);
+                        weigh(std::bool_constant<false>(), kk);
                     else
-                        weigh(PagedFlag<true>(), kk);
+                        weigh(std::bool_constant<true>(), kk);
                     uint32_t vb[4][D / 32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

@@ -642,9 +642,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                 };
                 if (was_whole)
-                    weigh(PagedFlag<false>());
+                    weigh(std::bool_constant<false>());
                 else
-                    weigh(PagedFlag<true>());
+                    weigh(std::bool_constant<true>());
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 fence_proxy_async_smem();
                 tc_fence_before_sync();

@@ -179,10 +179,15 @@ sdnq_status launch_chunk(const PagedParams &p, const DeviceInfo &dev, int sms, c
     return launch_status();
 }
 
-// Query rows of a kv head above which a sequence goes to the tensor-memory kernel. 16 sequences
-// of 4096 keys (32 heads over 8, 128), 36 rows: 94 us there, 101 us in three passes of the
-// other; 64 rows: 96 and 123 us; 24 rows: 69 us in two passes. (One sequence of 16384 keys is
-// still faster in passes at 64 rows: 50 and 46 us.)
+// Query rows of a kv head above which a sequence goes to the tensor-memory kernel; below, each
+// 16 rows are another pass over its keys. Measured with heads of 128, us there and in passes:
+//   16 sequences of 4096 keys, 32 heads over 8: 36 rows 92 and 135, 64 rows 93 and 166;
+//   one of 16384 keys:                          36 rows 49 and 50, 64 rows 50 and 57;
+//   one token each of 16 sequences of 4096, all heads on one kv head: 40 heads 39 and 42, 64 heads
+//   40 and 45, 128 heads 41 and 60.
+// One such sequence alone is faster in passes (16384 keys: 40 heads 49 and 33, 128 heads 52 and
+// 32; 131072 keys: 65 and 60, 68 and 86): the rule knows the rows of a sequence, not how many
+// segments there are, whose lengths are on the device.
 constexpr int32_t kPagedFewRows = 32;
 
 template <int D>
@@ -261,7 +266,6 @@ sdnq_status run_attention_paged(const uint16_t *q, int64_t ldq, int64_t T, int64
     p.pages = pages;
     p.T = static_cast<int32_t>(T);
     p.B = static_cast<int32_t>(B);
-    p.H = static_cast<int32_t>(H);
     p.Hkv = static_cast<int32_t>(Hkv);
     p.share = static_cast<int32_t>(H / Hkv);
     const int32_t bits = log2_of(p.share);   // division by the share as a product (rounded up)
