@@ -742,7 +742,7 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int | 
     (codes, scales): out [T, H, D] bf16. table [B, max_pages] int32 page ids, lens [B] int32
     tokens in the cache (the new ones included), cu_q [B + 1] int32 row offsets of the sequences
     (None: one new token each, T == B); max_q bounds the new tokens of a sequence and chooses the
-    kernels (None: 1 without cu_q, else T). Causal; with ``window`` > 0 a token sees the last
+    kernels (None: T, or 1 where there are no more rows than sequences). Causal; with ``window`` > 0 a token sees the last
     ``window`` keys and the first ``sinks``. ``ws``: uint8, attention_paged_workspace bytes."""
     dev = _device()
     T, H, D, ldq = _heads(q, "q", dev)
@@ -777,7 +777,7 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int | 
             raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     if max_q is None:
-        max_q = 1 if cu_q is None else max(T, 1)
+        max_q = T if T > B else 1
     _check(lib().sdnq_attention_paged(q.data_ptr(), ldq, T, H, cu, lens.data_ptr(), B, table.data_ptr(),
                                       width, ldt, codes.data_ptr(), scales.data_ptr(), pages, page, Hkv, D,
                                       int(max_q), group, scale, int(window), int(sinks), ws.data_ptr(),

@@ -96,3 +96,32 @@ def test_back_to_back_on_one_stream(D, page):
     torch.cuda.synchronize()
     for r, (x, y) in enumerate(zip(alone, together)):
         assert all(torch.equal(g, w) for g, w in zip(x, y)), r
+
+
+def test_a_captured_fork_with_memory_of_its_own():
+    """Two branches of one graph, on the capturing stream and on another that joined the capture, whose calls make
+    their workspaces and outputs themselves; replayed with other inputs and lengths."""
+    gpu, gl, gc, qs = setup(128, [3000, 900, 64], [150, 1, 40], 101)
+    ones = [ref.queries(3, 8, 128, 110 + i).cuda() for i in range(3)]
+    q, one = qs[0].clone(), ones[0].clone()
+    chunk = lambda **kw: sd.sdnq_attention_paged(q, *gpu, gl, cu_q=gc, max_q=150, **kw)           # noqa: E731
+    single = lambda **kw: sd.sdnq_attention_paged(one, *gpu, gl, window=500, sinks=3, **kw)       # noqa: E731
+    chunk(), single()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        a, b = chunk(), [single(stream=side) for _ in range(2)]
+        c = single()
+        here.wait_stream(side)
+    for i in range(3):
+        q.copy_(qs[i])
+        one.copy_(ones[i])
+        gl.copy_(torch.tensor([3000 - 700 * i, 900 + 5 * i, 64]))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (a, *b, c)]
+        want = [chunk(), single(), single(), single()]
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), i

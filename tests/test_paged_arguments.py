@@ -37,9 +37,11 @@ MAX_Q = 16   # its place among the library call's arguments
 
 
 @pytest.mark.parametrize("T,cu,given,want", [(3, False, None, 1), (300, True, None, 300), (0, True, None, 1),
-                                             (300, True, 7, 7), (300, True, 1, 1), (3, False, 5, 5)])
+                                             (300, True, 7, 7), (300, True, 1, 1), (3, False, 5, 5),
+                                             (3, True, None, 1), (2, True, None, 1), (4, True, None, 4)])
 def test_the_bound_on_new_tokens(calls, T, cu, given, want):
-    """A caller who gives offsets and no bound has chunks of up to T tokens, not single ones."""
+    """A caller who gives offsets and no bound may have chunks of up to T tokens; one with no more rows than sequences
+    has single ones."""
     sd.sdnq_attention_paged(bf(T, 4, 64), CODES, SCALES, i32(3, 7), i32(3), cu_q=i32(4) if cu else None,
                             **({} if given is None else {"max_q": given}))
     (name, args), = calls
