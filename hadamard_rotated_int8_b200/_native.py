@@ -742,8 +742,9 @@ def sdnq_attention_paged(q, codes, scales, table, lens, cu_q=None, max_q: int | 
     (codes, scales): out [T, H, D] bf16. table [B, max_pages] int32 page ids, lens [B] int32
     tokens in the cache (the new ones included), cu_q [B + 1] int32 row offsets of the sequences
     (None: one new token each, T == B); max_q bounds the new tokens of a sequence and chooses the
-    kernels (None: T, or 1 where there are no more rows than sequences). Causal; with ``window`` > 0 a token sees the last
-    ``window`` keys and the first ``sinks``. ``ws``: uint8, attention_paged_workspace bytes."""
+    kernels (None: T, or 1 where there are no more rows than sequences). Causal; with ``window``
+    > 0 a token sees the last ``window`` keys and the first ``sinks``. ``ws``: uint8,
+    attention_paged_workspace bytes."""
     dev = _device()
     T, H, D, ldq = _heads(q, "q", dev)
     pages, Hkv, page, Dc = _cache(codes, scales, dev)
