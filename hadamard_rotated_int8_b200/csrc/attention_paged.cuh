@@ -8,7 +8,9 @@
 // softmax; the values' rotation is undone once per output row. A row that sees no key is 0.
 #pragma once
 
+#include <cfloat>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -341,7 +343,7 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
 //   ring stays full while a segment is being finished;
 // - 4 warps take 32 keys of each tile each, with their own running maximum, sum and output:
 //   S^T = k q^T in int8 (m16n8k32), the exponentials, P^T moved into operand form
-//   (movmatrix), and O^T += v^T (p s_v) with v's codes turned into bf16 in registers
+//   (movmatrix), and O^T += v^T (p s_v) with v's codes turned into f16 in registers
 //   (m16n8k16). They meet only at the end of a segment.
 // Keys and dims, not query rows, fill the 16 rows of each instruction: with 8 query rows half
 // the instructions and accumulators of the other way round (64 sequences of up to 8192 keys, 32
@@ -393,27 +395,42 @@ struct FewDesc {       // the segment that begins in a block and goes on behind 
     int32_t r0;        // first (token, head) row of the tile
 };
 
-__device__ __forceinline__ void mma_m16n8k16_bf16(float (&d)[4], uint32_t a0, uint32_t a1,
+__device__ __forceinline__ void mma_m16n8k16_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                                                   uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3},"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3},"
                  " {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Byte `j` of a and of b, two int8 codes, as a bf16 pair (a low), exactly, times 2^-6. With
-// u = code + 128, the bf16 pattern 0x00uu is u 2^-133 (subnormal numbers and the first binade
-// have one spacing), so one fused multiply-add gives u 2^-6 - 2.
-constexpr float kCodeUnit = 64.0f;
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t a, uint32_t b, int j)
+// Byte `j` of a and of b, two int8 codes, as an f16 pair (a low), exactly: with u = code + 128, the
+// f16 pattern 0x64uu is 1024 + u.
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t a, uint32_t b, int j)
 {
     const uint32_t pick = static_cast<uint32_t>(j) * 0x1111u + 0x4400u;
     // bytes a_j, a_j, b_j, b_j
-    const uint32_t t = (__byte_perm(a, b, pick) & 0x00ff00ffu) ^ 0x00800080u;
+    const uint32_t t = (__byte_perm(a, b, pick) & 0x00ff00ffu) ^ 0x64806480u;
     uint32_t r;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(t), "r"(0x7f007f00u), "r"(0xc000c000u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0xe480e480u));   // - 1152
     return r;
+}
+
+// Weights. A key's weight in the product with V is w = 2^(y - R) s_v, y its logit (base 2) and R its
+// row's reference, in f16: 11 bits, within a range that R keeps. R moves (and the sums with it) when
+// a key the row sees would exceed 2^kWeightTop, and then leaves that key kWeightLag bits below; so
+// weights down to 2^-21 of the largest keep all bits, and what is below 2^-31 of it is lost. The
+// output's error is then that of its own rounding (relative to 64 bits 0.00166; with weights in
+// bf16, whose range needs no care, 0.00225). Two bf16 operands for a weight gave 0.00165, but 107
+// us for 64 sequences of up to 8192 keys (bf16 102.5, f16 103.2).
+// Since R follows log2 s_v, value scales may have any size. Where R is concerned they count as
+// kLeastScale at least: the sums of 2^(y - R) over rows of zeros must not overflow.
+constexpr float kWeightTop = 15.0f, kWeightLag = 8.0f, kLeastScale = 0x1p-80f;
+__device__ __forceinline__ float weight_room(float sv)   // log2 s_v, and down to where R puts a key
+{
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(fminf(fmaxf(fabsf(sv), kLeastScale), FLT_MAX)));
+    return r - (kWeightTop - kWeightLag);
 }
 
 __device__ __forceinline__ uint4 lds_u4(uint32_t addr)
@@ -734,27 +751,33 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                                 y[nb][kb][c] = see ? y[nb][kb][c] : -INFINITY;
                             }
                 }
-                // the sums are rescaled only when a row's maximum grows by more than 2^8
-                float mx[NB][2];
+                float sv[4];   // of keys 8 kb + PI(g)
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb)
+                    sv[kb] = lds_f(sc + (my_row[kb >> 1] + 8u * (kb & 1) + pp + krow_n) * 4u);
+                // whether a weight may be too large: the largest logit with the largest scale
+                const float room = weight_room(fmaxf(max3f(fabsf(sv[0]), fabsf(sv[1]), fabsf(sv[2])), fabsf(sv[3])));
                 bool grew = false;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        mx[nb][c] = fmaxf(max3f(y[nb][0][c], y[nb][1][c], y[nb][2][c]), y[nb][3][c]) * row_f[nb][c];
-                        grew |= mx[nb][c] > m[nb][c] + 8.0f;
-                    }
+                    for (int c = 0; c < 2; ++c)
+                        grew |= __fmaf_rn(fmaxf(max3f(y[nb][0][c], y[nb][1][c], y[nb][2][c]), y[nb][3][c]), row_f[nb][c],
+                                          room) > m[nb][c] + kWeightLag;
                 if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         float alpha[2];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float mb = mx[nb][c];
+                            float mb = -INFINITY;   // key by key; hidden keys have no part
+#pragma unroll
+                            for (int kb = 0; kb < 4; ++kb)
+                                mb = fmaxf(mb, __fmaf_rn(y[nb][kb][c], row_f[nb][c], weight_room(sv[kb])));
 #pragma unroll
                             for (int x = 4; x < 32; x <<= 1)
                                 mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
-                            const bool grow = mb > m[nb][c] + 8.0f;
+                            const bool grow = mb > m[nb][c] + kWeightLag;
                             alpha[c] = grow ? ex2_approx(m[nb][c] - mb) : 1.0f;
                             m[nb][c] = grow ? mb : m[nb][c];
                             l[nb][c] *= alpha[c];
@@ -766,15 +789,10 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                         }
                     }
                 }
-                // probabilities times s_v: keys PI(2t), PI(2t + 1), query row g; what their rounding to bf16
-                // leaves is a second operand of the same products. So o keeps 16 bits of them: its error is
-                // that of its own rounding (relative to 64 bits 0.00165 where one operand gives 0.00225; 64
-                // sequences of up to 8192 keys take 105 instead of 102 us)
-                uint32_t pb[NB][2], pl[NB][2];
-                auto weigh = [&](auto masked, int kk) {
+                uint32_t pb[NB][4];   // weights: keys PI(2t), PI(2t + 1), query row g
+                auto weigh = [&](auto masked) {
 #pragma unroll
-                    for (int kb = 2 * kk; kb < 2 * kk + 2; ++kb) {
-                        const float sv = lds_f(sc + (my_row[kb >> 1] + 8u * (kb & 1) + pp + krow_n) * 4u);
+                    for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             float pr[2];
@@ -783,27 +801,23 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                                 const float neg_m = m[nb][c] == -INFINITY ? 0.0f : -m[nb][c];
                                 const float x = ex2_approx(__fmaf_rn(y[nb][kb][c], row_f[nb][c], neg_m));
                                 l[nb][c] += x;
-                                pr[c] = x * sv;
+                                pr[c] = x * sv[kb];
                                 // a hidden key adds 0 whatever its scale holds
                                 if (decltype(masked)::value)
                                     pr[c] = y[nb][kb][c] == -INFINITY ? 0.0f : pr[c];
                             }
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(pr[0], pr[1]);
-                            const uint32_t hi = *reinterpret_cast<const uint32_t *>(&h2);
-                            const __nv_bfloat162 l2 = __floats2bfloat162_rn(pr[0] - __uint_as_float(hi << 16),
-                                                                            pr[1] - __uint_as_float(hi & 0xffff0000u));
-                            pb[nb][kb & 1] = movmatrix_trans(hi);
-                            pl[nb][kb & 1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&l2));
+                            const __half2 h2 = __floats2half2_rn(pr[0], pr[1]);
+                            pb[nb][kb] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h2));
                         }
                     }
                 };
+                if (whole)
+                    weigh(std::bool_constant<false>());
+                else
+                    weigh(std::bool_constant<true>());
                 // values of keys PI(2t), PI(2t + 1) of two 8-key blocks, this lane's D / 8 dims
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    if (whole)
-                        weigh(std::bool_constant<false>(), kk);
-                    else
-                        weigh(std::bool_constant<true>(), kk);
                     uint32_t vb[4][D / 32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -823,12 +837,10 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
                         uint32_t a[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            a[i] = codes_to_bf16x2(vb[i & 2][j >> 1], vb[(i & 2) + 1][j >> 1], (2 * j + (i & 1)) & 3);
+                            a[i] = codes_to_f16x2(vb[i & 2][j >> 1], vb[(i & 2) + 1][j >> 1], (2 * j + (i & 1)) & 3);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pb[nb][0], pb[nb][1]);
-                            mma_m16n8k16_bf16(o[nb][j], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
-                        }
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma_m16n8k16_f16(o[nb][j], a[0], a[1], a[2], a[3], pb[nb][2 * kk], pb[nb][2 * kk + 1]);
                     }
                 }
             }
@@ -862,7 +874,7 @@ __global__ void __launch_bounds__(kFewThreads, FewConfig<D, NB>::PER_SM)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     mm = fmaxf(mm, ml[i * ROWS + 8 * nb + 2 * t + c].x);
-                scale_o[nb][c] = m[nb][c] == -INFINITY ? 0.0f : kCodeUnit * ex2_approx(m[nb][c] - mm);
+                scale_o[nb][c] = m[nb][c] == -INFINITY ? 0.0f : ex2_approx(m[nb][c] - mm);
             }
         // o[nb][j][c], o[nb][j][2 + c]: dims 2j, 2j + 1 of the lane's, query row 8 nb + 2t + c
 #pragma unroll 1
