@@ -348,7 +348,7 @@ __device__ __forceinline__ void find_share(const PagedParams &p, int64_t blocks,
 // Keys and dims, not query rows, fill the 16 rows of each instruction: with 8 query rows half
 // the instructions and accumulators of the other way round (64 sequences of up to 8192 keys, 32
 // heads over 8 of 128: 103 against 138 us). Three blocks an SM with two stages for 8 rows, two
-// blocks with three stages for 16: what the registers allow. That case now takes 102 us, 5.6
+// blocks with three stages for 16: what the registers allow. That case now takes 103 us, 5.5
 // TB/s; one token over 131071 keys 55 us (floor 42), about 10 us of it the start, the join and
 // the tail.
 //
