@@ -406,8 +406,8 @@ sdnq_status sdnq_kv_read(const int64_t *slots, int64_t T, const int8_t *codes, c
  *   row as sdnq_kv_write makes them; o = butterfly(sum_j softmax(logit)_j * s_v[j] * vc_j) * c.
  *   Maxima, sums and accumulators are fp32, o is rounded to bf16. Probabilities times s_v enter
  *   the product with vc in f16 (11 bits; below 2^-31 of a row's largest they are lost), or in
- *   bf16 (8 bits) for sequences of more than 32 query rows (new tokens times H / Hkv) a kv head
- *   where max_q allows as many.
+ *   bf16 (8 bits, for s_v up to 2^100) for sequences of more than 32 query rows (new tokens times
+ *   H / Hkv) a kv head where max_q allows as many.
  *   A row that sees no key gives zeros; one whose query is not finite (as for sdnq_kv_write)
  *   gives NaN where it sees a key. What lies in slots a row does not see (uninitialised codes,
  *   infinite or NaN scales) has no effect on it.
